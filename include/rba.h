@@ -471,6 +471,143 @@ rba_status rba_decode_step_host(const rba_store* store, const void* q_host, void
                                 float* out_host, float* lse_host, int32_t* idx_host,
                                 void* workspace, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged 4-bit memory: the same decode attention for a batch of requests of different
+ * lengths, with K and V held in 4 bits ([IL] overall framework: sink, retrieved units and
+ * local window; a unit is one page).  Lengths, page tables and the free list live on the
+ * device and every call reads them there, so a sequence of calls can be captured in a graph
+ * and replayed while the requests grow.
+ *
+ * A page holds page_size tokens of one request for every kv head, in strips of 16 tokens
+ * (the last strip of a page may be part empty).  P = rba_row_pitch(D), G = P / 32:
+ *   pool  device, [n_pages][Hkv][ceil(page_size / 16)][rba_paged_strip_bytes(D)] bytes
+ *   a strip, 16 P + 64 G bytes (4.5 bits an element):
+ *     K codes  at 0:     32-bit word (token t, c < 4, group g) at word (4 t + c) G + g;
+ *                        its nibble j (low first) is dim 32 g + 8 c + j
+ *     V codes  at 8 P:   16-bit unit (token t = 8 p + 2 c + o, l < 8, group g) at unit
+ *                        ((8 p + l) 4 + c) 2 G + 2 g + o;  nibble j is dim 32 g + 4 l + j
+ *     scales   at 16 P:  bf16 [16][K groups 0 .. G-1, V groups 0 .. G-1]
+ *   Group g is dims 32 g .. 32 g + 31 (zeros past D).  With a = max |x| of a group,
+ *   s = bf16(a / 7), 0 where that is below 2^-100, NaN where a group holds a value that is not
+ *   finite; a nibble is c + 8 with c = rint(x * fl(1 / s)) clamped to -7 .. 7 (0 where s is 0 or
+ *   NaN), all in correctly rounded 32-bit arithmetic.  It stands for the value s c.
+ *
+ * Candidates: page j of a request of T tokens is a candidate when it is full and meets
+ * [sink, w0), w0 = min(max(T - window, 0), page_size * (T / page_size)): the window always
+ * covers a partial last page.  The attended set is sink U selected pages U window, each token
+ * once.  A request of no tokens is a valid one.
+ *
+ * Rows of q and of new K / V have dense dims and any row strides (in elements).  Calls that
+ * change a store (extend, truncate, append) are ordered by the caller against each other and
+ * against its readers, as work on one stream is; read, select and attend may overlap one
+ * another when each has its own workspace.  Lengths or page numbers out of range are skipped
+ * and flagged as RBA_ERR_BOUNDS in the status word (rba_paged_check). */
+typedef struct {
+  int32_t n_q_heads;    /* Hq, a multiple of n_kv_heads */
+  int32_t n_kv_heads;   /* Hkv */
+  int32_t head_dim;     /* D: a multiple of 4 up to 128 */
+  int32_t page_size;    /* tokens of a page >= 1 (a multiple of 16 wastes no row) */
+  int32_t n_pages;      /* pages the pool holds; n_pages * page_size < 2^31 */
+  int32_t max_requests; /* rows of the table, at most 4096 */
+  int32_t max_pages;    /* columns of the table; max_pages * page_size < 2^31 */
+  rba_dtype dtype;      /* q, new K / V rows and rows read back */
+} rba_paged_desc;
+
+/* Caller-owned device memory of a paged store. */
+typedef struct {
+  void* pool;           /* as above, 16-byte aligned */
+  float* rep;           /* fp32 [n_pages][Hkv][P], 16-byte aligned: mean of each full page's stored keys */
+  int32_t* table;       /* [max_requests][max_pages] page numbers */
+  int32_t* lens;        /* [max_requests] tokens each request holds; zeros at the start */
+  int32_t* free_pages;  /* [n_pages], a stack: the first *n_free are free; all pages at the start */
+  int32_t* n_free;      /* [1] */
+  int32_t* status;      /* [8], zeroed by the caller: as rba_store's status word, and scratch */
+} rba_paged_buffers;
+
+typedef struct rba_paged rba_paged;
+
+/* Host only, launches nothing.  Errors: INVALID_ARG, UNSUPPORTED. */
+rba_status rba_paged_create(const rba_paged_desc* desc, const rba_paged_buffers* buffers,
+                            rba_paged** out);
+rba_status rba_paged_destroy(rba_paged* store);
+int32_t rba_paged_strip_bytes(int32_t head_dim);  /* -1 for a head dim that is not held */
+
+/* Page tables and slot maps from request lengths.  Request r < n_requests grows by n_new[r]
+ * tokens: it takes the pages it lacks from the top of the free list (requests in order, pages
+ * ascending), and its new token i, at position lens[r] + i, gets
+ *   slots[starts[r] + i] = page * page_size + position % page_size.
+ * starts is the exclusive prefix sum of n_new; slots from starts[n_requests] on are -1 (a
+ * fixed n_slots serves every step of a replayed graph).  lens, table and the free list are
+ * updated.  A call that cannot be served whole (free pages, table columns or n_slots too few,
+ * a negative count) changes none of them: every slot is -1, starts are zero, and
+ * RBA_ERR_BOUNDS is flagged.
+ *   n_new device int32 [n_requests];  slots device int32 [n_slots];
+ *   starts device int32 [n_requests + 1]
+ * Errors: INVALID_ARG, CUDA. */
+rba_status rba_paged_extend(rba_paged* store, const int32_t* n_new, int32_t n_requests,
+                            int32_t* slots, int32_t n_slots, int32_t* starts,
+                            cudaStream_t stream);
+
+/* Cuts request r < n_requests back to min(lens[r], keep[r]) tokens (0: the request is over) and
+ * returns the pages past them to the free list, in the order that undoes an extension.
+ *   keep device int32 [n_requests], not negative (else nothing changes, RBA_ERR_BOUNDS flagged)
+ * Errors: INVALID_ARG, CUDA. */
+rba_status rba_paged_truncate(rba_paged* store, const int32_t* keep, int32_t n_requests,
+                              cudaStream_t stream);
+
+/* Writes n rows of K and V in 4 bits at their slots (-1: skipped; a slot past the pool is
+ * skipped and flagged), then the rep row of every page whose last row is among them: the mean
+ * of the page's stored keys.
+ *   slots device int32 [n], distinct (a slot given twice holds a mixture of its rows)
+ *   k, v  device dtype: row (i, h) at k + i * k_token_stride + h * k_head_stride, D elements
+ * Errors: INVALID_ARG, UNSUPPORTED (more rows than a grid holds), CUDA. */
+rba_status rba_paged_append(rba_paged* store, const int32_t* slots, int32_t n, const void* k,
+                            int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                            int64_t v_token_stride, int64_t v_head_stride, cudaStream_t stream);
+
+/* Rows at n slots as the values they stand for (zeros for -1 and for a slot past the pool,
+ * which is flagged).  Slots may repeat.
+ *   k, v  device dtype [n][Hkv][D], 16-byte aligned
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+rba_status rba_paged_read(const rba_paged* store, const int32_t* slots, int32_t n, void* k,
+                          void* v, cudaStream_t stream);
+
+/* The k best candidate pages of each (request, kv head): score = fp32 of the sum over dims, held
+ * in 64 bits, of (sum over the group's q heads of q) * rep; larger first, ties to the lower page.
+ *   q    device dtype, rows (r, head) as above, r < n_requests
+ *   idx  device int32 [n_requests][Hkv][k], written: pages of the request (columns of its table
+ *        row) ascending; -1 past its candidates
+ *   workspace >= rba_paged_select_workspace_size() (no contents are kept in it)
+ * NaN scores are not supported.  Errors: INVALID_ARG, UNSUPPORTED (more than 16384 candidates
+ * in max_pages), WORKSPACE, CUDA. */
+rba_status rba_paged_select(const rba_paged* store, const void* q, int64_t q_request_stride,
+                            int64_t q_head_stride, int32_t n_requests, int32_t k, int32_t sink,
+                            int32_t window, int32_t* idx, void* workspace, size_t ws_bytes,
+                            cudaStream_t stream);
+size_t rba_paged_select_workspace_size(const rba_paged* store);
+
+/* Decode attention of one token of each request r < n_requests over its attended set:
+ *   out = sum_t softmax_t(scale * q . k_t) v_t, lse the natural log of the sum;
+ * zeros and -infinity for a request of no tokens.
+ *   idx  device int32 [n_requests][Hkv][k] as rba_paged_select writes it (NULL when k = 0): the
+ *        first min(k, candidates) entries, distinct, are attended; others are not read.  An
+ *        entry that is no candidate is skipped and flagged.  k = 0 with a window of at least
+ *        every length attends to all tokens.
+ *   out  device fp32 [n_requests][Hq][D];  lse device fp32 [n_requests][Hq] or NULL
+ *   workspace >= rba_paged_attend_workspace_size(), 16-byte aligned, zeroed before the first
+ *        call (every call leaves its synchronisation words zero)
+ * Errors: INVALID_ARG, UNSUPPORTED (n_requests * max_pages * strips of a page >= 2^30),
+ * WORKSPACE, CUDA. */
+rba_status rba_paged_attend(const rba_paged* store, const void* q, int64_t q_request_stride,
+                            int64_t q_head_stride, int32_t n_requests, const int32_t* idx,
+                            int32_t k, int32_t sink, int32_t window, float scale, float* out,
+                            float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream);
+size_t rba_paged_attend_workspace_size(const rba_paged* store);
+
+/* As rba_store_check: synchronises `stream`, returns the first device-side error since the last
+ * check and clears it. */
+rba_status rba_paged_check(const rba_paged* store, cudaStream_t stream);
+
 /* Synchronises `stream`, reads the store's status word, clears it, and returns
  * the first device-side error recorded since the last check (RBA_OK if none). */
 rba_status rba_store_check(const rba_store* store, cudaStream_t stream);

@@ -1,0 +1,115 @@
+// Paged 4-bit memory: what its kernels share (the strip layout, a request's
+// candidate and strip geometry, block scans).
+//
+// A strip is 16 tokens of one (page, kv head), P = 64 or 128 dims a row in
+// G = P / 32 groups of one scale each.  It is laid out for the attention kernel's
+// matrix fragments, so that a lane's share of it is a few 16-byte loads:
+//   K codes  [token 16][c 4][group G] 32-bit words; nibble j is dim 32 g + 8 c + j
+//   V codes  [half 2][lane 8][c 4][group G][odd 2] 16-bit units of token
+//            8 half + 2 c + odd; nibble j is dim 32 g + 4 lane + j
+//   scales   [token 16][K groups G, V groups G] bf16
+#pragma once
+
+#include "rba_internal.cuh"
+
+struct rba_paged {
+  rba_paged_desc d;
+  rba_paged_buffers b;
+  int32_t pitch;   // P
+  int32_t strips;  // strips of one (page, kv head): ceil(page_size / 16)
+};
+
+namespace rba {
+
+constexpr int kStrip = 16;           // tokens of a strip
+constexpr int kMaxRequests = 4096;   // rows of a page table (scanned in one CTA's shared memory)
+constexpr int kPagedMaxCandidates = 16384;  // scores one CTA selects from in shared memory
+
+__host__ __device__ constexpr int strip_groups(int P) { return P / 32; }
+__host__ __device__ constexpr int strip_bytes(int P) { return 16 * P + 64 * strip_groups(P); }
+// byte offsets inside a strip
+template <int P> __device__ __forceinline__ int k_unit_at(int t, int g, int lane) {
+  // 16-bit unit of dims 32 g + 4 lane .. + 3 of token t
+  return ((t * 4 + (lane >> 1)) * (P / 32) + g) * 4 + (lane & 1) * 2;
+}
+template <int P> __device__ __forceinline__ int v_unit_at(int t, int g, int lane) {
+  const int half = t >> 3, c = (t & 7) >> 1, odd = t & 1;
+  return 8 * P + (((half * 8 + lane) * 4 + c) * (P / 32) + g) * 4 + odd * 2;
+}
+template <int P> __device__ __forceinline__ int scale_at(int t, int which, int g) {
+  return 16 * P + (t * 2 * (P / 32) + which * (P / 32) + g) * 2;
+}
+
+// One request's attended set, in strips.  Page j is a candidate when it is full and
+// meets [sink, w0); the window always covers the partial last page.
+struct PagedGeo {
+  int T, w0, sink_end, first, nc;
+};
+__host__ __device__ inline PagedGeo paged_geo(int T, int bs, int sink, int window) {
+  PagedGeo g;
+  const int full = T / bs;
+  const int open = T > window ? T - window : 0;
+  g.T = T;
+  g.w0 = open < full * bs ? open : full * bs;
+  g.sink_end = sink < g.w0 ? sink : g.w0;
+  g.first = sink / bs;
+  int hi = g.w0 / bs + (g.w0 % bs != 0);
+  hi = hi < full ? hi : full;
+  g.nc = hi > g.first ? hi - g.first : 0;
+  return g;
+}
+
+// A request's length as the store holds it; a length outside the table is reported and
+// taken as 0.
+__device__ __forceinline__ int paged_len(const int32_t* lens, int r, int bs, int max_pages,
+                                         int32_t* status) {
+  const int T = lens[r];
+  if (T < 0 || T > int64_t(max_pages) * bs) {
+    report(status, RBA_ERR_BOUNDS, kWherePaged, r);
+    return 0;
+  }
+  return T;
+}
+
+// Exclusive block scan of one 64-bit value a thread (every thread calls it); *total is
+// the sum.  s_w holds one word per warp.
+__device__ __forceinline__ int64_t block_scan64(int64_t v, int64_t* s_w, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+  int64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) s_w[warp] = incl;
+  __syncthreads();
+  int64_t base = 0, tot = 0;
+  for (int w = 0; w < nw; ++w) {
+    const int64_t x = s_w[w];
+    if (w < warp) base += x;
+    tot += x;
+  }
+  __syncthreads();
+  *total = tot;
+  return base + incl - v;
+}
+
+// Largest i in [0, n) with pre[i] <= x, for a non-decreasing pre with pre[0] <= x.
+template <typename T>
+__device__ __forceinline__ int last_at_most(const T* pre, int n, T x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Top k per row of scores [rows][row_stride], row = request * heads + kv head: the request's
+// candidates only, written as page numbers ascending, then -1.
+rba_status launch_topk_paged(const float* scores, int row_stride, int rows, int heads,
+                             const int32_t* lens, int bs, int max_pages, int sink, int window,
+                             int k, int32_t* idx, cudaStream_t stream);
+
+}  // namespace rba

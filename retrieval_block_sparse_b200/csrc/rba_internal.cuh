@@ -44,6 +44,7 @@ enum Where : int32_t {
   kWhereFused = 6,
   kWhereMemory = 7,
   kWhereStep = 8,
+  kWherePaged = 9,
 };
 
 __device__ __forceinline__ void report(int32_t* status, int32_t code, int32_t where,

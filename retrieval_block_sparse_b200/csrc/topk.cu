@@ -9,6 +9,7 @@
 // radix select where that does not apply); longer rows go through a
 // multi-CTA radix select.
 #include "rba_internal.cuh"
+#include "paged.cuh"
 #include "topk_impl.cuh"
 
 namespace rba {
@@ -272,7 +273,47 @@ __global__ void __launch_bounds__(kRowThreads) topk_rows_kernel(const float* __r
                  s_misc);
 }
 
+// The same for the rows of a paged memory, each as long as its request has candidates; a row
+// with fewer than k of them is filled up with -1.
+__global__ void __launch_bounds__(kRowThreads) topk_paged_rows_kernel(
+    const float* __restrict__ scores, int row_stride, int heads, const int32_t* __restrict__ lens,
+    int bs, int max_pages, int sink, int window, int k, int32_t* __restrict__ idx) {
+  extern __shared__ __align__(16) char sm[];
+  float* vals = reinterpret_cast<float*>(sm);                               // [row_stride]
+  uint8_t* flag = reinterpret_cast<uint8_t*>(sm + size_t(row_stride) * 4);  // [row_stride]
+  __shared__ int cand[kRowThreads];
+  __shared__ uint32_t hist[kBins];
+  __shared__ int s_w[32];
+  __shared__ int s_misc[8];
+  __shared__ float s_f[2 * kRowWarps];
+  const int64_t row = blockIdx.x;
+  const int len = lens[row / heads];
+  const PagedGeo g =
+      paged_geo(len < 0 || len > int64_t(max_pages) * bs ? 0 : len, bs, sink, window);
+  const int n = min(g.nc, row_stride);
+  const float* s = scores + row * row_stride;
+  int32_t* dst = idx + row * k;
+  if (k >= n) {
+    for (int j = threadIdx.x; j < k; j += kRowThreads) dst[j] = j < n ? g.first + j : -1;
+    return;
+  }
+  if (!select_binned(s, n, k, g.first, dst, vals, flag, cand, hist, s_w, s_misc, s_f))
+    select_radix(s, n, k, g.first, dst, reinterpret_cast<uint32_t*>(vals), flag, hist, s_w,
+                 s_misc);
+}
+
 }  // namespace
+
+rba_status launch_topk_paged(const float* scores, int row_stride, int rows, int heads,
+                             const int32_t* lens, int bs, int max_pages, int sink, int window,
+                             int k, int32_t* idx, cudaStream_t stream) {
+  const size_t smem = size_t(row_stride) * 5 + 16;
+  RBA_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(topk_paged_rows_kernel), smem));
+  topk_paged_rows_kernel<<<rows, kRowThreads, smem, stream>>>(
+      scores, row_stride, heads, lens, bs, max_pages, sink, window, k, idx);
+  RBA_LAUNCH_CHECK();
+  return RBA_OK;
+}
 
 rba_status launch_topk(const float* scores, int rows, int n, int k, int index_base, int32_t* idx,
                        void* ws, size_t ws_bytes, cudaStream_t stream, bool pdl) {

@@ -67,6 +67,20 @@ SIGNATURES = {
                                    ctypes.POINTER(_c_i64), _p]),
     "rba_decode_step_host": (_c_i32, [_p, _p, _p, _c_i32, _c_i64, _c_i32, _c_i32, _c_f32, _p, _p,
                                       _p, _p, _p, _p, _p, _c_size, _p]),
+    "rba_paged_create": (_c_i32, [_p, _p, ctypes.POINTER(_p)]),
+    "rba_paged_destroy": (_c_i32, [_p]),
+    "rba_paged_strip_bytes": (_c_i32, [_c_i32]),
+    "rba_paged_extend": (_c_i32, [_p, _p, _c_i32, _p, _c_i32, _p, _p]),
+    "rba_paged_truncate": (_c_i32, [_p, _p, _c_i32, _p]),
+    "rba_paged_append": (_c_i32, [_p, _p, _c_i32, _p, _c_i64, _c_i64, _p, _c_i64, _c_i64, _p]),
+    "rba_paged_read": (_c_i32, [_p, _p, _c_i32, _p, _p, _p]),
+    "rba_paged_select": (_c_i32, [_p, _p, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _p, _p,
+                                  _c_size, _p]),
+    "rba_paged_select_workspace_size": (_c_size, [_p]),
+    "rba_paged_attend": (_c_i32, [_p, _p, _c_i64, _c_i64, _c_i32, _p, _c_i32, _c_i32, _c_i32,
+                                  _c_f32, _p, _p, _p, _c_size, _p]),
+    "rba_paged_attend_workspace_size": (_c_size, [_p]),
+    "rba_paged_check": (_c_i32, [_p, _p]),
     "rba_store_check": (_c_i32, [_p, _p]),
     "rba_row_pitch": (_c_i32, [_c_i32]),
     "rba_status_string": (ctypes.c_char_p, [_c_i32]),
@@ -461,6 +475,216 @@ class Store:
     def check(self):
         """Synchronises and raises if a kernel recorded a device-side error."""
         _check(lib().rba_store_check(self.handle, _stream()), "device status")
+
+
+class _PagedDesc(ctypes.Structure):
+    _fields_ = [("n_q_heads", _c_i32), ("n_kv_heads", _c_i32), ("head_dim", _c_i32),
+                ("page_size", _c_i32), ("n_pages", _c_i32), ("max_requests", _c_i32),
+                ("max_pages", _c_i32), ("dtype", _c_i32)]
+
+
+class _PagedBuffers(ctypes.Structure):
+    _fields_ = [(n, _p) for n in ("pool", "rep", "table", "lens", "free_pages", "n_free",
+                                  "status")]
+
+
+class PagedStore:
+    """A paged memory in 4 bits for requests of different lengths (rba_paged_* in rba.h).
+
+    A page is a memory block of `page_size` tokens.  Lengths, page tables and the free list
+    live on the device and are read there by every call, so a decode step (extend, append,
+    select, attend) can be captured once and replayed while the requests grow.
+
+    Buffers (allocated here, or the caller's own where given; contiguous, on one device):
+      pool    uint8 [n_pages][Hkv][strips][strip_bytes]   rep   fp32 [n_pages][Hkv][P]
+      table   int32 [max_requests][max_pages]             lens  int32 [max_requests]
+      free    int32 [n_pages] (a stack)                   n_free int32 [1]
+    Work runs on the store's device, on torch's current stream there.
+    """
+
+    def __init__(self, *, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
+                 max_pages, dtype="bf16", device="cuda", pool=None, rep=None, table=None,
+                 lens=None, free=None, n_free=None):
+        self.dtype = BF16 if dtype in ("bf16", torch.bfloat16) else F32
+        self.Hq, self.Hkv, self.D, self.page_size = n_q_heads, n_kv_heads, head_dim, page_size
+        self.n_pages, self.max_requests, self.max_pages = n_pages, max_requests, max_pages
+        L = lib()
+        self.pitch = L.rba_row_pitch(head_dim)
+        if self.pitch < 0:
+            raise RbaError(ERR_UNSUPPORTED, f"head_dim {head_dim}")
+        self.strip_bytes = L.rba_paged_strip_bytes(head_dim)
+        strips = -(-page_size // 16) if page_size > 0 else 0
+        given = [t for t in (pool, rep, table, lens, free, n_free) if t is not None]
+        dev = given[0].device if given else torch.device(device)
+
+        def buf(name, t, shape, dt, fill):
+            if t is None:
+                return fill(shape, dt)
+            if tuple(t.shape) != shape or t.dtype != dt or t.device != dev:
+                raise ValueError(f"{name}: expected {dt} {shape} on {dev}, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+            _ptr(t)
+            return t
+
+        def zeros(shape, dt):
+            return torch.zeros(shape, dtype=dt, device=dev)
+
+        if (free is None) != (n_free is None):
+            raise ValueError("free and n_free are given together")
+        self.pool = buf("pool", pool, (n_pages, n_kv_heads, strips, self.strip_bytes),
+                        torch.uint8, zeros)
+        self.rep = buf("rep", rep, (n_pages, n_kv_heads, self.pitch), torch.float32, zeros)
+        self.table = buf("table", table, (max_requests, max_pages), torch.int32, zeros)
+        self.lens = buf("lens", lens, (max_requests,), torch.int32, zeros)
+        self.free = buf("free", free, (n_pages,), torch.int32,
+                        lambda s, dt: torch.arange(n_pages - 1, -1, -1, dtype=dt, device=dev))
+        self.n_free = buf("n_free", n_free, (1,), torch.int32,
+                          lambda s, dt: torch.full(s, n_pages, dtype=dt, device=dev))
+        self.device = self.pool.device
+        self.status = zeros((8,), torch.int32)
+        d = _PagedDesc(n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
+                       max_pages, self.dtype)
+        b = _PagedBuffers(*(_ptr(t) for t in (self.pool, self.rep, self.table, self.lens,
+                                              self.free, self.n_free, self.status)))
+        h = _p()
+        with torch.cuda.device(self.device):
+            _check(L.rba_paged_create(ctypes.byref(d), ctypes.byref(b), ctypes.byref(h)),
+                   "rba_paged_create")
+        self.handle = h
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and _LIB is not None:
+            _LIB.rba_paged_destroy(h)
+            self.handle = None
+
+    @property
+    def tdtype(self):
+        return _tdtype(self.dtype)
+
+    # -- marshalling -----------------------------------------------------------
+    def _call(self, name, *args):
+        """One library call on the store's device and torch's current stream there."""
+        i = self.device.index
+        stream = torch.cuda.current_stream(i).cuda_stream
+        if torch.cuda.current_device() == i:
+            s = getattr(_LIB, name)(self.handle, *args, stream)
+        else:
+            with torch.cuda.device(i):
+                s = getattr(_LIB, name)(self.handle, *args, stream)
+        if s != OK:
+            raise RbaError(s, name)
+
+    def _arg(self, name, t, shape, dt):
+        """Pointer of a contiguous tensor of exactly this shape, type and device."""
+        if t.dtype != dt or tuple(t.shape) != shape or t.device != self.device:
+            raise ValueError(f"{name}: expected {dt} {shape} on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous tensor")
+        return t.data_ptr()
+
+    def _rows(self, name, t, n, heads):
+        """(pointer, row stride, head stride) of rows [n][heads][D] with dense dims."""
+        if t.dtype != self.tdtype or tuple(t.shape) != (n, heads, self.D) or \
+                t.device != self.device:
+            raise ValueError(f"{name}: expected {self.tdtype} {(n, heads, self.D)} on "
+                             f"{self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        sn, sh, sd = t.stride()
+        if sd != 1 and self.D > 1:
+            raise ValueError(f"{name}: the head dim must be dense")
+        return t.data_ptr(), sn, sh
+
+    # -- page tables -------------------------------------------------------------
+    def extend(self, n_new, n_slots, *, slots=None, starts=None):
+        """Grows request r by n_new[r] tokens.  Returns (slots [n_slots], -1 past the new
+        tokens; starts [R + 1], the first new token of each request)."""
+        R = n_new.shape[0]
+        if slots is None:
+            slots = torch.empty(n_slots, dtype=torch.int32, device=self.device)
+        if starts is None:
+            starts = torch.empty(R + 1, dtype=torch.int32, device=self.device)
+        self._call("rba_paged_extend", self._arg("n_new", n_new, (R,), torch.int32), R,
+                   self._arg("slots", slots, (n_slots,), torch.int32), n_slots,
+                   self._arg("starts", starts, (R + 1,), torch.int32))
+        return slots, starts
+
+    def truncate(self, keep):
+        """Cuts request r back to at most keep[r] tokens (0: the request is over)."""
+        R = keep.shape[0]
+        self._call("rba_paged_truncate", self._arg("keep", keep, (R,), torch.int32), R)
+
+    # -- rows ----------------------------------------------------------------------
+    def append(self, slots, k, v):
+        """Writes rows k, v [n][Hkv][D] in 4 bits at their slots, and the mean keys of the
+        pages they complete.  Rows may be strided views (a fused projection's slices)."""
+        n = slots.shape[0]
+        kp, kt, kh = self._rows("k", k, n, self.Hkv)
+        vp, vt, vh = self._rows("v", v, n, self.Hkv)
+        self._call("rba_paged_append", self._arg("slots", slots, (n,), torch.int32), n, kp, kt,
+                   kh, vp, vt, vh)
+
+    def read(self, slots, *, k=None, v=None):
+        """Rows at the slots as the values held there: (k, v), each [n][Hkv][D]."""
+        n = slots.shape[0]
+        shape = (n, self.Hkv, self.D)
+        if k is None:
+            k = torch.empty(shape, dtype=self.tdtype, device=self.device)
+        if v is None:
+            v = torch.empty(shape, dtype=self.tdtype, device=self.device)
+        self._call("rba_paged_read", self._arg("slots", slots, (n,), torch.int32), n,
+                   self._arg("k", k, shape, self.tdtype), self._arg("v", v, shape, self.tdtype))
+        return k, v
+
+    # -- select, attend --------------------------------------------------------------
+    def select_workspace(self):
+        n = lib().rba_paged_select_workspace_size(self.handle)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
+
+    def select(self, q, k, sink, window, *, idx=None, workspace=None):
+        """The k best pages of each (request, kv head) for q [R][Hq][D]: idx [R][Hkv][k],
+        ascending, -1 past a request's candidates."""
+        R = q.shape[0]
+        qp, qr, qh = self._rows("q", q, R, self.Hq)
+        if idx is None:
+            idx = torch.empty((R, self.Hkv, k), dtype=torch.int32, device=self.device)
+        if workspace is None:
+            workspace = self.select_workspace()
+        self._call("rba_paged_select", qp, qr, qh, R, k, sink, window,
+                   self._arg("idx", idx, (R, self.Hkv, k), torch.int32), workspace.data_ptr(),
+                   workspace.numel())
+        return idx
+
+    def attend_workspace(self):
+        """Zeroed workspace of attend; one serves every call, one call at a time."""
+        with torch.cuda.device(self.device):
+            n = lib().rba_paged_attend_workspace_size(self.handle)
+        return torch.zeros(max(n, 16), dtype=torch.uint8, device=self.device)
+
+    def attend(self, q, idx, sink, window, *, scale=None, out=None, lse=None, workspace=None):
+        """Attention of one token of each request, q [R][Hq][D], over its sink tokens, the
+        pages idx (None: no pages) and its window.  Returns (out fp32 [R][Hq][D], lse)."""
+        R = q.shape[0]
+        qp, qr, qh = self._rows("q", q, R, self.Hq)
+        k = idx.shape[-1] if idx is not None else 0
+        ip = self._arg("idx", idx, (R, self.Hkv, k), torch.int32) if k else None
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.D)
+        if out is None:
+            out = torch.empty((R, self.Hq, self.D), dtype=torch.float32, device=self.device)
+        if lse is None:
+            lse = torch.empty((R, self.Hq), dtype=torch.float32, device=self.device)
+        if workspace is None:
+            workspace = self.attend_workspace()
+        self._call("rba_paged_attend", qp, qr, qh, R, ip, k, sink, window, scale,
+                   self._arg("out", out, (R, self.Hq, self.D), torch.float32),
+                   self._arg("lse", lse, (R, self.Hq), torch.float32), workspace.data_ptr(),
+                   workspace.numel())
+        return out, lse
+
+    def check(self):
+        """Synchronises and raises if a kernel recorded a device-side error."""
+        self._call("rba_paged_check")
 
 
 def memory_rule(n):

@@ -1,0 +1,617 @@
+"""The paged 4-bit memory on the GPU against the oracle: page tables and slot maps, quantised
+rows bit by bit, selections exactly, attention in fp64.
+
+Tolerance of attention, in units of 2^-24 of U, the largest sum of |products| behind a logit
+(PagedModel.attend): q is held as two 11-bit halves (4 units), each group's two matrix products
+and their sum are rounded or cut at 2^-23 (2 x 2 + 2 units a group, at most 4 groups folded by
+sums that each add one: bounded by 12 in all since the groups' parts add up to U), the factor
+(scale * log2 e * 2^n) and its product 4: at most 24.  An error x of a logit moves a weight by the
+factor e^x, so an output by at most 2 x of the largest |v|; the weights' halves, exp2 and the
+normalisation add 8 units of 2^-22, and each strip summed one more of 2^-23 (cut accumulators)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+
+
+def bf16(x):
+    return O.round_bf16(x)
+
+
+def cuda(x, dtype="f32"):
+    t = torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda()
+    return t.bfloat16() if dtype == "bf16" else t
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def rows(r, shape, dtype="f32"):
+    x = r.normal(size=shape).astype(np.float32)
+    return bf16(x) if dtype == "bf16" else x
+
+
+class Pair:
+    """A store and its model, driven by the same calls."""
+
+    def __init__(self, rba, seed, *, heads=2, group=2, dim=128, page=16, n_pages=64, requests=3,
+                 columns=24, dtype="bf16"):
+        self.r = np.random.default_rng(seed)
+        self.dtype, self.heads, self.group, self.dim, self.page = dtype, heads, group, dim, page
+        self.m = O.PagedModel(heads, dim, page, n_pages, requests, columns)
+        self.st = rba.PagedStore(n_q_heads=heads * group, n_kv_heads=heads, head_dim=dim,
+                                 page_size=page, n_pages=n_pages, max_requests=requests,
+                                 max_pages=columns, dtype=dtype)
+
+    def grow(self, new, pad=3, k=None, v=None):
+        total = sum(new)
+        slots, starts = self.st.extend(i32(new), total + pad)
+        want = self.m.extend(new, total + pad)
+        assert slots.tolist() == want + [-1] * pad
+        assert starts.tolist() == [0] + np.cumsum(new).tolist()
+        k = rows(self.r, (total + pad, self.heads, self.dim), self.dtype) if k is None else k
+        v = rows(self.r, (total + pad, self.heads, self.dim), self.dtype) if v is None else v
+        self.st.append(slots, cuda(k, self.dtype), cuda(v, self.dtype))
+        self.m.append(want, k, v)
+        self.same_tables()
+        return slots
+
+    def same_tables(self):
+        assert self.st.lens.tolist() == self.m.lens
+        n = int(self.st.n_free)
+        assert self.st.free[:n].tolist() == self.m.free
+        for r, t in enumerate(self.m.tables):
+            assert self.st.table[r, :len(t)].tolist() == t
+
+    def queries(self, scale=1.0):
+        q = rows(self.r, (len(self.m.lens), self.heads * self.group, self.dim), self.dtype) * \
+            np.float32(scale)
+        return q, cuda(q, self.dtype)
+
+    def same_attention(self, q, qd, idx, sink, window, scale=None, **kw):
+        scale = self.dim ** -0.5 if scale is None else scale
+        out, lse = self.st.attend(qd, None if idx is None else i32(idx), sink, window, scale=scale,
+                                  **kw)
+        self.st.check()
+        ref, rl, vmax, unit = self.m.attend(q, idx, sink, window, scale)
+        strips = max(self.m.lens) / 16 + 1
+        dx = 24 * unit * 2.0 ** -24
+        tol = vmax * (2 * dx + 8 * 2.0 ** -22 + strips * 2.0 ** -23)
+        err = np.abs(out.cpu().numpy() - ref).max()
+        assert err <= tol, (err, tol)
+        seen = np.isfinite(rl)
+        got = lse.cpu().numpy()
+        assert np.array_equal(np.isneginf(got), ~seen)
+        top = np.abs(rl[seen]).max() if seen.any() else 0
+        assert np.abs(got[seen] - rl[seen]).max(initial=0) <= dx + (top + 4) * 2.0 ** -22
+        return out, lse
+
+
+# ---------------------------------------------------------------------------------------------
+# tables
+
+@pytest.mark.parametrize("requests,page,biggest", [(1, 1, 5), (3, 7, 40), (40, 16, 300),
+                                                   (1025, 3, 9), (4096, 2, 3)])
+def test_tables_follow_the_model(rba, requests, page, biggest):
+    r = np.random.default_rng(requests)
+    n_pages = requests * (-(-4 * biggest // page))
+    m = O.PagedModel(1, 4, page, n_pages, requests, -(-4 * biggest // page))
+    st = rba.PagedStore(n_q_heads=1, n_kv_heads=1, head_dim=4, page_size=page, n_pages=n_pages,
+                        max_requests=requests, max_pages=m.columns)
+    for step in range(8):
+        if step % 3 == 2:
+            keep = [int(r.integers(0, n + 2)) for n in m.lens]
+            st.truncate(i32(keep))
+            m.truncate(keep)
+        else:
+            new = r.integers(0, biggest + 1, requests) * (r.random(requests) < 0.7)
+            new = [int(min(x, m.columns * page - n)) for x, n in zip(new, m.lens)]
+            slots, starts = st.extend(i32(new), sum(new) + step)
+            want = m.extend(new, sum(new) + step)
+            assert want is not None
+            assert slots.tolist() == want + [-1] * step
+            assert starts.tolist() == np.concatenate([[0], np.cumsum(new)]).tolist()
+        st.check()
+        assert st.lens.tolist() == m.lens
+        n = int(st.n_free)
+        assert n == len(m.free) and st.free[:n].tolist() == m.free
+        table = st.table.cpu().numpy()
+        for i, t in enumerate(m.tables):
+            assert table[i, :len(t)].tolist() == t
+
+
+def test_tables_of_fewer_requests_leave_the_others(rba):
+    p = Pair(rba, 1, requests=4)
+    p.grow([5, 20, 3, 30])
+    slots, _ = p.st.extend(i32([1, 12]), 13)
+    p.m.tables, rest = p.m.tables[:2], p.m.tables[2:]
+    want = p.m.extend([1, 12], 13)
+    p.m.tables += rest
+    assert slots.tolist() == want
+    p.same_tables()
+    p.st.truncate(i32([2]))
+    assert p.st.lens.tolist() == [2, 32, 3, 30]
+
+
+@pytest.mark.parametrize("new,n_slots", [([40, 0, 0], 50), ([9, 9, 9], 26), ([-1, 2, 0], 9),
+                                         ([2 ** 31 - 1, 2 ** 31 - 1, 5], 9), ([13, 12, 1], 30)])
+def test_refused_extension_changes_nothing(rba, new, n_slots):
+    # 6 pages of 8 and 4 columns: too long a request, too few slots, a negative and an enormous
+    # count, more pages than are free
+    st = rba.PagedStore(n_q_heads=1, n_kv_heads=1, head_dim=64, page_size=8, n_pages=6,
+                        max_requests=3, max_pages=4)
+    st.extend(i32([8, 9, 0]), 17)
+    before = [t.clone() for t in (st.lens, st.n_free, st.free, st.table)]
+    slots, starts = st.extend(i32(new), n_slots)
+    assert slots.tolist() == [-1] * n_slots and starts.tolist() == [0] * 4
+    assert all(torch.equal(a, b) for a, b in zip(before, (st.lens, st.n_free, st.free, st.table)))
+    with pytest.raises(rba.RbaError) as e:
+        st.check()
+    assert e.value.status == rba.ERR_BOUNDS
+    st.check()  # cleared
+
+
+def test_refused_truncation_changes_nothing(rba):
+    st = rba.PagedStore(n_q_heads=1, n_kv_heads=1, head_dim=64, page_size=8, n_pages=6,
+                        max_requests=2, max_pages=4)
+    st.extend(i32([8, 9]), 17)
+    before = [t.clone() for t in (st.lens, st.n_free, st.free)]
+    st.truncate(i32([0, -1]))
+    assert all(torch.equal(a, b) for a, b in zip(before, (st.lens, st.n_free, st.free)))
+    with pytest.raises(rba.RbaError):
+        st.check()
+
+
+# ---------------------------------------------------------------------------------------------
+# rows
+
+SHAPES = [(2, 128, 16, "bf16"), (1, 64, 16, "f32"), (3, 100, 50, "f32"), (2, 36, 7, "bf16"),
+          (2, 96, 1, "bf16"), (1, 4, 24, "f32"), (5, 128, 33, "f32")]
+
+
+@pytest.mark.parametrize("heads,dim,page,dtype", SHAPES)
+def test_rows_are_stored_bit_by_bit(rba, heads, dim, page, dtype):
+    p = Pair(rba, dim + page, heads=heads, dim=dim, page=page, dtype=dtype, n_pages=40,
+             columns=40)
+    kept = {}
+    p.st.pool.fill_(0xA5)  # what no row covers stays as it was
+    for new in ([3, 0, page], [1, page + 1, 0], [2 * page, 1, 1]):
+        k, v = (rows(p.r, (sum(new) + 3, heads, dim), dtype) * np.float32(3) for _ in range(2))
+        if dtype == "bf16":
+            k, v = bf16(k), bf16(v)
+        slots = p.grow(new, k=k, v=v).tolist()
+        kept.update({s: (k[i], v[i]) for i, s in enumerate(slots) if s >= 0})
+    p.st.check()
+    pool = p.st.pool.cpu().numpy()
+    P = p.st.pitch
+    for page_no in range(40):
+        for h in range(heads):
+            for s in range(-(-page // 16)):
+                own = [kept.get(page_no * page + s * 16 + t) if s * 16 + t < page else None
+                       for t in range(16)]
+                image, mask = O.strip_image(
+                    *([None if x is None else O.quantise_row(x[w][h]) for x in own]
+                      for w in (0, 1)), P)
+                want = (image & mask) | (0xA5 & ~mask)
+                assert np.array_equal(pool[page_no, h, s], want), (page_no, h, s)
+    rep = p.st.rep.cpu().numpy()
+    assert p.m.reps
+    for page_no in range(40):
+        if page_no in p.m.reps:
+            # a mean of `page` stored values in 32 bits: page + 2 roundings of at most |value|
+            top = np.abs([p.m.rows[page_no * page + i][0] for i in range(page)]).max()
+            err = np.abs(rep[page_no, :, :dim] - p.m.reps[page_no]).max()
+            assert err <= top * (page + 2) * 2.0 ** -24
+            assert not rep[page_no, :, dim:].any()
+        else:
+            assert not rep[page_no].any()
+    # read back, in any order, with repeats and none
+    order = p.r.permutation(list(kept)).tolist()[:37]
+    order = order + [-1] + order[:2]
+    k, v = p.st.read(i32(order))
+    for got, w in ((k, 0), (v, 1)):
+        want = np.stack([p.m.rows[s][w] if s >= 0 else np.zeros((heads, dim)) for s in order])
+        want = torch.from_numpy(want).float().to(got.dtype)  # (c s fits 32 bits: 4 + 8 bits)
+        assert torch.equal(got.cpu(), want)
+
+
+def test_special_values(rba):
+    p = Pair(rba, 9, heads=1, dim=128, page=16, dtype="f32", requests=1)
+    k = rows(p.r, (8, 1, 128))
+    k[0, 0, :32] = 0
+    k[1, 0, 40] = np.inf
+    k[2, 0, 70] = np.nan
+    k[3, 0, 96:] = 2.0 ** -104          # below the least scale
+    k[4, 0, :32] = 3.0e38               # near the largest
+    k[5, 0, 32:64] = 0
+    k[5, 0, 33] = 2.0 ** -95            # a lone small value keeps its scale
+    k[6, 0] = -k[4, 0]
+    k[7, 0, :32] = np.arange(-16, 16)   # halves: ties to even
+    p.grow([8], pad=0, k=k, v=k[::-1].copy())
+    got, v = p.st.read(i32(list(range(8))))
+    want = np.stack([O.row_values(*O.quantise_row(x[0])) for x in k])
+    np.testing.assert_array_equal(got[:, 0].cpu().numpy().astype(np.float64), want)
+    np.testing.assert_array_equal(v[:, 0].cpu().numpy().astype(np.float64), want[::-1])
+    assert np.isnan(want[1, 32:64]).all() and np.isfinite(want[1, :32]).all()
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f32", 100), ("bf16", 36)])
+def test_strided_rows(rba, dtype, dim):
+    # slices of a fused projection, an odd head stride, a view that starts off a boundary
+    heads, n = 2, 20
+    p = Pair(rba, 4, heads=heads, dim=dim, dtype=dtype, requests=1)
+    a, b, c = (rba.PagedStore(n_q_heads=4, n_kv_heads=heads, head_dim=dim, page_size=16,
+                              n_pages=4, max_requests=1, max_pages=4, dtype=dtype)
+               for _ in range(3))
+    k, v = (cuda(rows(p.r, (n, heads, dim), dtype), dtype) for _ in range(2))
+    slots = a.extend(i32([n]), n)[0]
+    a.append(slots, k, v)
+    fused = torch.zeros((n, 3, heads, dim), dtype=k.dtype, device="cuda")
+    fused[:, 1], fused[:, 2] = k, v
+    b.append(slots, fused[:, 1], fused[:, 2])
+    odd = torch.zeros(n * heads * (dim + 1) + 1, dtype=k.dtype, device="cuda")
+    kk = odd[1:].view(n, heads, dim + 1)[..., :dim]
+    kk.copy_(k)
+    c.append(slots, kk, v.flip(0).flip(0))
+    assert torch.equal(a.pool, b.pool) and torch.equal(a.pool, c.pool)
+    assert torch.equal(a.rep, b.rep) and torch.equal(a.rep, c.rep)
+
+
+def test_slots_past_the_pool_are_flagged(rba):
+    st = rba.PagedStore(n_q_heads=1, n_kv_heads=1, head_dim=64, page_size=4, n_pages=2,
+                        max_requests=1, max_pages=2)
+    x = torch.ones((3, 1, 64), device="cuda").bfloat16()
+    st.append(i32([-1, 8, 2 ** 31 - 1]), x, x)
+    assert not st.pool.any() and not st.rep.any()
+    with pytest.raises(rba.RbaError):
+        st.check()
+    k, _ = st.read(i32([8, 0]))
+    assert not k.any()
+    with pytest.raises(rba.RbaError):
+        st.check()
+
+
+def test_empty_calls(rba):
+    st = rba.PagedStore(n_q_heads=2, n_kv_heads=1, head_dim=64, page_size=4, n_pages=2,
+                        max_requests=2, max_pages=2)
+    e = torch.empty((0, 1, 64), dtype=torch.bfloat16, device="cuda")
+    slots, starts = st.extend(i32([0, 0]), 0)
+    assert slots.numel() == 0 and starts.tolist() == [0, 0, 0]
+    st.append(slots, e, e)
+    assert st.read(slots)[0].shape == (0, 1, 64)
+    q = torch.ones((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    idx = st.select(q, 3, 0, 0)
+    assert (idx == -1).all()
+    out, lse = st.attend(q, idx, 4, 4)
+    assert not out.any() and torch.isneginf(lse).all()
+    st.check()
+
+
+# ---------------------------------------------------------------------------------------------
+# selection
+
+@pytest.mark.parametrize("heads,group,dim,page,dtype,lens,k,sink,window", [
+    (2, 4, 128, 16, "bf16", [700, 0, 130, 47], 5, 16, 40),
+    (1, 1, 64, 7, "f32", [400, 6, 7, 8], 3, 0, 0),
+    (3, 2, 100, 50, "f32", [1049, 300], 6, 60, 33),
+    (2, 16, 128, 8, "bf16", [600], 64, 4, 16),
+    (1, 5, 96, 1, "f32", [200, 33], 17, 3, 9),
+    (2, 1, 36, 24, "bf16", [24 * 30, 23, 24, 25], 40, 1000, 1)])
+def test_selection_is_the_models(rba, heads, group, dim, page, dtype, lens, k, sink, window):
+    p = Pair(rba, k, heads=heads, group=group, dim=dim, page=page, dtype=dtype,
+             n_pages=sum(-(-n // page) for n in lens) + 1, requests=len(lens),
+             columns=-(-max(lens) // page) + 2)
+    p.grow(lens)
+    # the definition starts from the stored means
+    rep = p.st.rep.cpu().numpy().astype(np.float64)
+    p.m.reps = {n: rep[n, :, :dim] for n in p.m.reps}
+    q, qd = p.queries()
+    got = p.st.select(qd, k, sink, window)
+    p.st.check()
+    assert np.array_equal(got.cpu().numpy(), p.m.select(q, k, sink, window))
+
+
+def test_selection_ties_go_to_the_lower_page(rba):
+    p = Pair(rba, 3, heads=1, group=1, dim=64, page=4, dtype="f32", requests=1, columns=40)
+    p.grow([100])
+    p.st.rep.copy_(torch.round(p.st.rep * 2))       # whole numbers: many equal scores
+    p.st.rep[p.st.table[0, 5:9].long()] = p.st.rep[p.st.table[0, 20].long()].clone()
+    p.m.reps = {n: p.st.rep[n, :, :64].cpu().numpy().astype(float) for n in p.m.reps}
+    q = np.round(p.r.normal(size=(1, 1, 64)) * 2).astype(np.float32)
+    for k in (1, 2, 3, 7, 24):
+        got = p.st.select(cuda(q), k, 0, 0)
+        assert np.array_equal(got.cpu().numpy(), p.m.select(q, k, 0, 0)), k
+
+
+# ---------------------------------------------------------------------------------------------
+# attention
+
+ATTEND = [
+    # heads, group, dim, page, dtype, lens, k, sink, window
+    (2, 4, 128, 16, "bf16", [500, 1, 0, 130], 4, 16, 40),
+    (2, 1, 128, 50, "bf16", [333, 49, 50, 51, 100], 2, 0, 21),
+    (1, 2, 64, 64, "f32", [61], 0, 64, 128),
+    (1, 8, 128, 16, "f32", [300, 17], 3, 5, 33),
+    (2, 5, 100, 24, "f32", [200, 0, 25], 2, 30, 7),
+    (1, 16, 128, 8, "bf16", [150, 9], 5, 3, 4),
+    (1, 7, 36, 33, "f32", [400], 3, 50, 60),
+    (1, 12, 64, 7, "bf16", [130, 64], 4, 0, 0),
+    (3, 3, 96, 1, "f32", [70, 2], 9, 2, 5),
+    (1, 4, 4, 16, "f32", [90], 2, 8, 16),
+    (2, 4, 128, 128, "bf16", [1500, 127, 128], 3, 200, 100),
+    (1, 4, 128, 16, "bf16", [16, 16, 16], 1, 0, 0),
+    (1, 1, 128, 16, "f32", [40], 2, 0, 1),
+    (1, 2, 64, 16, "bf16", [100, 3], 6, 2 ** 31 - 1, 2 ** 31 - 1),
+]
+
+
+def _attended(rba, seed, case):
+    heads, group, dim, page, dtype, lens, k, sink, window = case
+    p = Pair(rba, seed, heads=heads, group=group, dim=dim, page=page, dtype=dtype,
+             n_pages=sum(-(-n // page) for n in lens) + 1, requests=len(lens),
+             columns=-(-max(lens) // page) + 1)
+    p.st.pool.fill_(0xFF)  # codes 15 and NaN scales wherever no row is written
+    p.grow(lens)
+    idx = None
+    if k:
+        idx = np.full((len(lens), heads, k), 2 ** 30)  # past the candidates: never read
+        for r in range(len(lens)):
+            cand = p.m.parts(r, sink, window)[2]
+            for h in range(heads):
+                pick = sorted(p.r.permutation(cand)[:k].astype(int))
+                idx[r, h, :len(pick)] = pick
+    return p, idx, sink, window
+
+
+@pytest.mark.parametrize("case", ATTEND)
+def test_attention_matches_the_oracle(rba, case):
+    p, idx, sink, window = _attended(rba, 7, case)
+    q, qd = p.queries()
+    p.same_attention(q, qd, idx, sink, window)
+
+
+@pytest.mark.parametrize("case", [ATTEND[0], ATTEND[3], ATTEND[6]])
+def test_attention_over_all_tokens(rba, case):
+    p, _, _, _ = _attended(rba, 8, case)
+    q, qd = p.queries()
+    ws = p.st.attend_workspace()
+    a = p.same_attention(q, qd, None, 0, max(p.m.lens), workspace=ws)
+    b = p.same_attention(q, qd, None, 0, 2 ** 31 - 1, workspace=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # one head's rows alone are the same row by row, whatever the batch around them
+    assert not ws[: 4 * len(p.m.lens) * p.heads * -(-p.group // 4)].any()
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 3.0, -1.0])
+def test_attention_scales(rba, scale):
+    p, idx, sink, window = _attended(rba, 11, ATTEND[0])
+    q, qd = p.queries()
+    p.same_attention(q, qd, idx, sink, window, scale=scale)
+
+
+@pytest.mark.parametrize("qs,ks,vs", [(2.0 ** -60, 2.0 ** 60, 1.0), (2.0 ** 60, 2.0 ** -60, 2.0 ** 100),
+                                      (0.0, 1.0, 2.0 ** -90), (1.0, 0.0, 2.0 ** 60),
+                                      (2.0 ** 10, 2.0 ** -10, 2.0 ** -60)])
+def test_attention_ranges(rba, qs, ks, vs):
+    p = Pair(rba, 13, heads=1, group=4, dim=128, requests=1, dtype="f32")
+    k, v = (rows(p.r, (120, 1, 128)) * np.float32(x) for x in (ks, vs))
+    p.grow([120], pad=0, k=k, v=v)
+    q, qd = p.queries(qs)
+    p.same_attention(q, qd, None, 0, 120)
+
+
+def test_attention_value_scales_far_apart(rba):
+    # rows of values from 2^-40 to 2^40 in one request, the large ones with small weights and late
+    p = Pair(rba, 17, heads=1, group=4, dim=128, requests=1, dtype="f32", n_pages=64,
+             columns=40)
+    k, v = rows(p.r, (640, 1, 128)), rows(p.r, (640, 1, 128))
+    v *= np.float32(2.0) ** np.linspace(-40, 40, 640).astype(np.float32)[:, None, None]
+    p.grow([640], pad=0, k=k, v=v)
+    q, qd = p.queries()
+    p.same_attention(q, qd, None, 0, 640)
+    p2 = Pair(rba, 17, heads=1, group=4, dim=128, requests=1, dtype="f32", n_pages=64,
+             columns=40)
+    p2.grow([640], pad=0, k=k[::-1].copy(), v=v[::-1].copy())
+    p2.same_attention(q, qd, None, 0, 640)
+
+
+def test_attention_one_token_dominates(rba):
+    p = Pair(rba, 19, heads=2, group=4, dim=64, requests=1, dtype="f32", n_pages=64,
+             columns=40)
+    q, qd = p.queries()
+    k = rows(p.r, (500, 2, 64))
+    k[311] = q[0].reshape(2, 4, 64).mean(1) * 20   # found late: the reference has to move
+    k[20] = -k[311]
+    p.grow([500], pad=0, k=k)
+    p.same_attention(q, qd, None, 0, 500)
+
+
+def test_values_that_are_not_finite_stay_in_their_place(rba):
+    p = Pair(rba, 23, heads=2, group=2, dim=128, requests=2, dtype="f32")
+    k, v = rows(p.r, (80, 2, 128)), rows(p.r, (80, 2, 128))
+    v[10, 0, 40] = np.inf    # request 0, head 0, dims 32 .. 63
+    k[70, 1, 0] = np.nan     # request 1, head 1
+    p.grow([48, 32], pad=0, k=k, v=v)
+    out = p.st.attend(p.queries()[1], None, 0, 80)[0].cpu().numpy()
+    bad = np.zeros(out.shape, bool)
+    bad[0, :2, 32:64] = True
+    bad[1, 2:] = True
+    assert np.array_equal(np.isnan(out), bad) and np.isfinite(out[~bad]).all()
+    # outside the attended set they are not seen
+    out, lse = p.st.attend(p.queries()[1], None, 4, 5)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+
+
+def test_strided_queries(rba):
+    p, idx, sink, window = _attended(rba, 29, ATTEND[0])
+    q, qd = p.queries()
+    wide = torch.zeros((qd.shape[0], 3, qd.shape[1], qd.shape[2] + 8), dtype=qd.dtype, device="cuda")
+    view = wide[:, 1, :, 3:3 + qd.shape[2]]
+    view.copy_(qd)
+    a, b = (p.st.attend(x, i32(idx), sink, window) for x in (qd, view))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert torch.equal(p.st.select(qd, 3, sink, window), p.st.select(view, 3, sink, window))
+
+
+def test_bad_pages_and_lengths_are_skipped_and_flagged(rba):
+    p, idx, sink, window = _attended(rba, 31, ATTEND[0])
+    q, qd = p.queries()
+    good = p.st.attend(qd, i32(idx), sink, window)[0].clone()
+    p.st.check()
+    bad = idx.copy()
+    bad[0, 0, 1] = 999
+    out = p.st.attend(qd, i32(bad), sink, window)[0]
+    with pytest.raises(rba.RbaError):
+        p.st.check()
+    assert torch.equal(out[0, 4:], good[0, 4:]) and torch.isfinite(out).all()
+    p.st.table[3, 0] = p.st.n_pages
+    out = p.st.attend(qd, i32(idx), sink, window)[0]
+    p.st.select(qd, 2, sink, window)
+    with pytest.raises(rba.RbaError):
+        p.st.check()
+    assert torch.equal(out[0], good[0])
+    p.st.lens[1] = 2 ** 30
+    out = p.st.attend(qd, i32(idx), sink, window)[0]
+    with pytest.raises(rba.RbaError):
+        p.st.check()
+    # (one strip fewer cuts the line of strips elsewhere: other partial sums)
+    assert not out[1].any() and torch.allclose(out[0], good[0], rtol=0, atol=1e-4)
+
+
+def test_python_refusals(rba):
+    p = Pair(rba, 1)
+    q = p.queries()[1]
+    with pytest.raises(ValueError):
+        p.st.attend(q.float(), None, 0, 8)
+    with pytest.raises(ValueError):
+        p.st.attend(q[..., ::2].repeat(1, 1, 2)[..., ::2], None, 0, 8)
+    with pytest.raises(ValueError):
+        p.st.attend(q, torch.zeros((3, 2, 1), dtype=torch.int64, device="cuda"), 0, 8)
+    with pytest.raises(ValueError):
+        p.st.attend(q.cpu(), None, 0, 8)
+    with pytest.raises(ValueError):
+        p.st.extend(i32([1, 2, 3]).cpu(), 6)
+    with pytest.raises(ValueError):
+        p.st.append(i32([0]), q[:1], q[:1])
+    with pytest.raises(rba.RbaError):
+        p.st.attend(torch.cat([q, q]), None, 0, 8)  # more requests than the table has rows
+    with pytest.raises(rba.RbaError):
+        p.st.attend(q, None, 0, 8, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        rba.PagedStore(n_q_heads=1, n_kv_heads=1, head_dim=64, page_size=8, n_pages=2,
+                       max_requests=1, max_pages=2, lens=torch.zeros(2, dtype=torch.int32).cuda())
+
+
+# ---------------------------------------------------------------------------------------------
+# together
+
+def test_decode_steps_replayed_while_requests_grow(rba):
+    """One captured step (extend, append, select, attend) replayed over growing requests, one of
+    them idle, with a request that ends and starts again; every step against the model."""
+    requests, k, sink, window = 3, 2, 5, 20
+    p = Pair(rba, 41, heads=2, group=4, dim=64, page=8, n_pages=60, requests=requests, columns=24)
+    p.grow([70, 0, 33])
+    st = p.st
+    new = i32([1, 0, 1])
+    slots = torch.empty(4, dtype=torch.int32, device="cuda")
+    starts = torch.empty(requests + 1, dtype=torch.int32, device="cuda")
+    kv = torch.zeros((4, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((requests, 8, 64), dtype=torch.bfloat16, device="cuda")
+    idx = torch.empty((requests, 2, k), dtype=torch.int32, device="cuda")
+    out, lse = torch.empty((requests, 8, 64), device="cuda"), torch.empty((requests, 8), device="cuda")
+    ws, sws = st.attend_workspace(), st.select_workspace()
+
+    def step():
+        st.extend(new, 4, slots=slots, starts=starts)
+        st.append(slots, kv[:, 0], kv[:, 1])
+        st.select(q, k, sink, window, idx=idx, workspace=sws)
+        st.attend(q, idx, sink, window, out=out, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        saved = [t.clone() for t in (st.lens, st.n_free)]
+        step()  # a first call of each kernel before the capture
+        st.lens.copy_(saved[0])
+        st.n_free.copy_(saved[1])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(30):
+        grow = [1, int(i % 3 == 1), 1]
+        if i == 17:
+            st.truncate(i32([2 ** 31 - 1, 0, 40]))
+            p.m.truncate([2 ** 31 - 1, 0, 40])
+        new.copy_(i32(grow))
+        k_new, v_new, qn = (rows(p.r, s, "bf16") for s in ((4, 2, 64), (4, 2, 64), (3, 8, 64)))
+        kv.copy_(torch.stack([cuda(k_new), cuda(v_new)], 1))
+        q.copy_(cuda(qn))
+        graph.replay()
+        st.check()
+        want = p.m.extend(grow, 4)
+        assert slots.tolist() == want + [-1] * (4 - len(want))
+        p.m.append(want, k_new, v_new)
+        rep = st.rep.cpu().numpy().astype(np.float64)
+        p.m.reps = {n: rep[n] for n in p.m.reps}
+        sel = p.m.select(qn, k, sink, window)
+        assert np.array_equal(idx.cpu().numpy(), sel)
+        ref, rl, vmax, unit = p.m.attend(qn, sel, sink, window, 64 ** -0.5)
+        tol = vmax * (48 * unit * 2.0 ** -24 + 16 * 2.0 ** -22)
+        assert np.abs(out.cpu().numpy() - ref).max() <= tol
+        p.same_tables()
+
+
+def test_readers_on_two_streams(rba):
+    p, idx, sink, window = _attended(rba, 43, ATTEND[10])
+    q, qd = p.queries()
+    want = [t.clone() for t in p.st.attend(qd, i32(idx), sink, window)]
+    sel = p.st.select(qd, 3, sink, window).clone()
+    di = i32(idx)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [p.st.attend_workspace() for _ in streams]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        for s, w in zip(streams, ws):
+            with torch.cuda.stream(s):
+                got.append((*p.st.attend(qd, di, sink, window, workspace=w),
+                            p.st.select(qd, 3, sink, window)))
+    torch.cuda.synchronize()
+    for out, lse, s in got:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(s, sel)
+
+
+def test_long_request_split_over_every_cta(rba):
+    """20000 tokens of two heads: every unit is merged from many CTAs' parts; against torch in
+    64 bits on the rows read back."""
+    r = np.random.default_rng(5)
+    n, heads, group, dim = 20000, 2, 4, 128
+    st = rba.PagedStore(n_q_heads=8, n_kv_heads=heads, head_dim=dim, page_size=64, n_pages=320,
+                        max_requests=2, max_pages=320)
+    k, v = (cuda(rows(r, (n, heads, dim), "bf16"), "bf16") for _ in range(2))
+    slots = st.extend(i32([n - 77, 77]), n)[0]
+    st.append(slots, k, v)
+    q = cuda(rows(r, (2, 8, dim), "bf16"), "bf16")
+    out, lse = st.attend(q, None, 0, n)
+    st.check()
+    # (values as held, in 64 bits: the bf16 read-back would round them)
+    wide = rba.PagedStore(n_q_heads=8, n_kv_heads=heads, head_dim=dim, page_size=64, n_pages=320,
+                          max_requests=2, max_pages=320, dtype="f32", pool=st.pool, rep=st.rep,
+                          table=st.table, lens=st.lens, free=st.free, n_free=st.n_free)
+    K, V = (x.double() for x in wide.read(slots))
+    for i, (a, b) in enumerate(((0, n - 77), (n - 77, n))):
+        x = torch.einsum("hgd,thd->hgt", q[i].double().view(heads, group, dim), K[a:b]) * dim ** -0.5
+        ref = torch.einsum("hgt,thd->hgd", x.softmax(-1), V[a:b]).flatten(0, 1)
+        unit = (q[i].double().abs().sum(-1).max() * K.abs().max() * dim ** -0.5 * 15 / 7).item()
+        strips = (b - a) / 16 / (64 if i == 0 else 1)  # (each of a unit's warps sums a share)
+        tol = V.abs().max().item() * (48 * unit * 2.0 ** -24 + 8 * 2.0 ** -22 + strips * 2.0 ** -23)
+        assert (out[i].double() - ref).abs().max().item() <= tol
+        want = torch.logsumexp(x, -1).flatten()
+        assert (lse[i].double() - want).abs().max().item() <= 24 * unit * 2.0 ** -24 + 16 * 2.0 ** -22
