@@ -3,17 +3,16 @@
 // out = sum_t softmax_t(scale q . k_t) v_t over each request's sink tokens, selected pages and
 // window, K and V held as codes c (a nibble, c + 8) and bf16 scales s per 32 dims.
 //
-// Mathematics.  With Q_g = sum of q over group g's dims,
-//   q . k_t = sum_g s_tg (sum_d q_d (c_td + 8) - 8 Q_g),
-// so the inner sums run on the codes and the scales enter after them.  A nibble placed in the
-// low bits of a half-precision word IS a number, (c + 8) 2^-24 (a subnormal half; 2^-20 for the
-// nibble above it), so one AND turns a word of codes into an operand of mma.sync m16n8k16:
-// no conversion.  q is scaled by a power of two per head and split into two halves (hi + lo,
-// 22 bits), in neighbouring columns of the product: 8 columns are 4 q heads, exactly a GQA
-// group of 4.  For the values the weight takes the scale, w = p s_tg 2^e, again split into
-// hi + lo columns; the code is made signed there (one subtraction of halves, exact), since
-// -8 sum w would cancel against the sum when many tokens share the weight.  Softmax
-// statistics, both products' accumulators and the merges are 32-bit.
+// Mathematics.  q . k_t = sum_g s_tg sum_{d in g} q_d c_td, so the inner sums run on the codes
+// and a scale enters once per group.  A nibble masked out of a word of two half-precision numbers
+// is the number (c + 8) 2^-24 there (a subnormal half; 2^-20 for the nibble above it), and one
+// fused multiply-add of halves turns it into c 2^-9, exactly: an AND and an HFMA2 for two codes,
+// no conversion.  (Fed to the matrix unit as they are, subnormal operands cost it precision: it
+// aligns products by their nominal exponents, and the outputs were off by 2^-17.)  q is scaled by
+// a power of two per head and split into two halves (hi + lo, 22 bits), in neighbouring columns
+// of the product: 8 columns are 4 q heads, exactly a GQA group of 4.  For the values the weight
+// takes the scale, w = p s_tg 2^e, again split into hi + lo columns.  Softmax statistics, both
+// products' accumulators and the merges are 32-bit.
 //
 // Layout.  One warp takes a strip of 16 tokens: K codes are the A operand of the first product
 // (16 tokens x 16 dims), q its B; V codes, read in token pairs, are the A operand of the second
@@ -86,9 +85,16 @@ __device__ __forceinline__ float pow2(int n) { return __int_as_float((n + 127) <
 __device__ __forceinline__ int exponent(float x) {
   return static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 127;
 }
-__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
-  const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&d);
+// Two codes, 2^-9 each, from the nibbles that `mask` leaves: nibble 0 (or 1) of each half word.
+template <int kNibble>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  const uint32_t x = w & (kNibble ? 0x00f000f0u : 0x000f000fu);
+  const uint32_t up = kNibble ? 0x68006800u : 0x78007800u;  // 2^11 or 2^15, twice
+  const uint32_t off = 0xa400a400u;                         // -8 2^-9, twice
+  const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&x),
+                            *reinterpret_cast<const __half2*>(&up),
+                            *reinterpret_cast<const __half2*>(&off));
+  return *reinterpret_cast<const uint32_t*>(&y);
 }
 
 // A unit's strips as one line: sink, selected pages, window.
@@ -199,7 +205,6 @@ template <int P, int NT> struct State {
 template <int P, int NT>
 __device__ __forceinline__ void strip_step(const Frag<P>& f, bool whole, int ra, int rb,
                                            const uint32_t (&qf)[NT][P / 16][2],
-                                           const float (&bias)[NT][P / 32],
                                            const float (&fac)[NT], State<P, NT>& st) {
   constexpr int G = P / 32;
   const int lane = threadIdx.x & 31, t = lane >> 2;
@@ -209,20 +214,13 @@ __device__ __forceinline__ void strip_step(const Frag<P>& f, bool whole, int ra,
   for (int i = 0; i < NT; ++i) x[i][0] = x[i][1] = 0.f;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    uint32_t a0[4], a1[4];
-    const uint32_t w0 = f.k[0][g], w1 = f.k[1][g];
-    a0[0] = w0 & 0x000f000fu;
-    a0[1] = w1 & 0x000f000fu;
-    a0[2] = w0 & 0x00f000f0u;
-    a0[3] = w1 & 0x00f000f0u;
-    a1[0] = (w0 >> 8) & 0x000f000fu;
-    a1[1] = (w1 >> 8) & 0x000f000fu;
-    a1[2] = (w0 >> 8) & 0x00f000f0u;
-    a1[3] = (w1 >> 8) & 0x00f000f0u;
+    const uint32_t w0 = f.k[0][g], w1 = f.k[1][g], u0 = w0 >> 8, u1 = w1 >> 8;
+    const uint32_t a0[4] = {codes2<0>(w0), codes2<0>(w1), codes2<1>(w0), codes2<1>(w1)};
+    const uint32_t a1[4] = {codes2<0>(u0), codes2<0>(u1), codes2<1>(u0), codes2<1>(u1)};
     const float s0 = scale_of<G>(f.s[0], g), s1 = scale_of<G>(f.s[1], g);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      float d[4] = {bias[i][g], 0.f, bias[i][g], 0.f};
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
       mma16816(d, a0, qf[i][2 * g][0], qf[i][2 * g][1], d);
       mma16816(d, a1, qf[i][2 * g + 1][0], qf[i][2 * g + 1][1], d);
       x[i][0] = fmaf(s0, d[0] + d[1], x[i][0]);
@@ -291,15 +289,15 @@ __device__ __forceinline__ void strip_step(const Frag<P>& f, bool whole, int ra,
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    // codes of the group's two 16-dim tiles, signed
+    // codes of the group's two 16-dim tiles
     uint32_t a0[4], a1[4];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const uint32_t w = f.v[half][g];
-      a0[2 * half] = sub_half2(w & 0x000f000fu, 0x00080008u);
-      a0[2 * half + 1] = sub_half2(w & 0x00f000f0u, 0x00800080u);
-      a1[2 * half] = sub_half2((w >> 8) & 0x000f000fu, 0x00080008u);
-      a1[2 * half + 1] = sub_half2((w >> 8) & 0x00f000f0u, 0x00800080u);
+      const uint32_t w = f.v[half][g], u = w >> 8;
+      a0[2 * half] = codes2<0>(w);
+      a0[2 * half + 1] = codes2<1>(w);
+      a1[2 * half] = codes2<0>(u);
+      a1[2 * half + 1] = codes2<1>(u);
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -392,15 +390,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_attend_kernel
 
     // each head scaled by a power of two to a largest value in [2^14, 2^15)
     uint32_t qf[NT][P / 16][2];
-    float bias[NT][G], fac[NT];
+    float fac[NT];
     State<P, NT> st;
     st.e = 120;
     {
       const int t = lane >> 2, c = lane & 3;
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        // column t of the tile: head t / 2 of it, its hi (even) or lo part; this lane's bias
-        // and factor are those of head c
+        // column t of the tile: head t / 2 of it, its hi (even) or lo part; this lane's factor
+        // is that of head c
         float top[4];
 #pragma unroll
         for (int hh = 0; hh < 4; ++hh) {
@@ -424,24 +422,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_attend_kernel
           for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-              // nibbles 2 ks + b and + 4 of the word; the odd ones carry a factor of 2^4
+              // nibbles 2 ks + b and + 4 of the word
               const int d = 32 * g + 8 * c + 2 * ks + b;
-              const float down = b ? 0.0625f : 1.f;
-              const float x0 = row[d] * up0 * up1 * down, x1 = row[d + 4] * up0 * up1 * down;
+              const float x0 = row[d] * up0 * up1, x1 = row[d + 4] * up0 * up1;
               const float h0f = __half2float(__float2half_rn(x0));
               const float h1f = __half2float(__float2half_rn(x1));
               qf[i][2 * g + ks][b] = (t & 1) ? pack_half2(x0 - h0f, x1 - h1f) : pack_half2(h0f, h1f);
             }
-        const float cu0 = pow2(ec / 2), cu1 = pow2(ec - ec / 2);
-        const float* crow = qs + (i * 4 + c) * P;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float s = 0.f;
-#pragma unroll
-          for (int d = 0; d < 32; ++d) s += crow[32 * g + d] * cu0 * cu1;
-          bias[i][g] = -s * 0x1p-21f;  // -8 2^-24
-        }
-        fac[i] = a.scale * kLog2e * pow2((24 - ec) / 2) * pow2((24 - ec) - (24 - ec) / 2);
+        fac[i] = a.scale * kLog2e * pow2((9 - ec) / 2) * pow2((9 - ec) - (9 - ec) / 2);
         st.m[i] = -INFINITY;
         st.l[i] = 0.f;
 #pragma unroll
@@ -465,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_attend_kernel
         if (hi == 0) continue;
         Frag<P> f;
         load_frag<P>(strip, lane, f);
-        strip_step<P, NT>(f, lo == 0 && hi == kStrip, lo, hi, qf, bias, fac, st);
+        strip_step<P, NT>(f, lo == 0 && hi == kStrip, lo, hi, qf, fac, st);
       }
     }
 
@@ -484,10 +472,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_attend_kernel
           const float* d0 = st.acc[i][2 * g];
           const float* d1 = st.acc[i][2 * g + 1];
           float* o = s + 32 * g + 4 * t;
-          o[0] = (d0[0] + d0[1]) * 0x1p24f * down;
-          o[1] = (d0[2] + d0[3]) * 0x1p20f * down;
-          o[2] = (d1[0] + d1[1]) * 0x1p24f * down;
-          o[3] = (d1[2] + d1[3]) * 0x1p20f * down;
+          o[0] = (d0[0] + d0[1]) * 0x1p9f * down;
+          o[1] = (d0[2] + d0[3]) * 0x1p9f * down;
+          o[2] = (d1[0] + d1[1]) * 0x1p9f * down;
+          o[3] = (d1[2] + d1[3]) * 0x1p9f * down;
         }
         if (t == 0) {
           s[P] = st.m[i];
