@@ -13,7 +13,7 @@
 // takes the scale, w = p s_tg 2^e, split the same way.  Softmax statistics, both products'
 // accumulators and the merges are 32-bit.
 //
-// Layout.  One warp takes a strip of 16 tokens: K codes are the A operand of the first product
+// Layout.  One warp takes a pair of strips of 16 tokens at a time.  K codes are the A operand of the first product
 // (16 tokens x 16 dims), q its B; V codes, read in token pairs, are the A operand of the second
 // (16 dims x 16 tokens), and the weights its B after 8 x 8 transposes in registers.  Up to four
 // q heads to a kv head fill the eight columns with their hi and lo halves ("packed": one product
@@ -23,8 +23,8 @@
 // The running maximum is lazy: weights are taken relative to a reference that moves only when
 // a logit passes it by 2^4, so most strips need no cross-lane maximum and no rescale.
 //
-// Work.  All strips of all (request, kv head) units form one line, cut evenly over the CTAs
-// whatever the requests' lengths; warps take a CTA's strips in turn, each through its own ring
+// Work.  All pairs of strips of all (request, kv head) units form one line, cut evenly over the
+// CTAs whatever the requests' lengths; warps take a CTA's pairs in turn, each through its own ring
 // of bulk copies, which runs on across units.  A CTA's part of a unit that it does not hold
 // whole goes to the workspace, and the last of the unit's CTAs to arrive merges the parts in
 // order.
@@ -39,12 +39,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 4;           // strips in flight per warp
-constexpr int kLeast = 2 * kWarps;   // strips a CTA takes at least (or a whole unit)
+constexpr int kStages = 2;           // pairs of strips in a warp's ring
+constexpr int kLeast = kWarps;       // pairs a CTA takes at least (or a whole unit)
 constexpr float kToLog2 = 1.4426950408889634f;
 constexpr float kToLn = 0.6931471805599453f;
 constexpr float kSlack = 4.f;        // a logit may pass the reference by 2^4
 constexpr int kScaleTop = 10;        // s 2^e stays below 2^10 when e is set, below 2^11 always
+constexpr int kMostE = 100, kLeastE = -118;
 
 struct PagedAttendArgs {
   const void* q;
@@ -73,6 +74,13 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, const uint
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+__device__ __forceinline__ void mma16816_first(float* d, const uint32_t* a, const uint32_t* b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -161,43 +169,24 @@ __device__ __forceinline__ const uint8_t* locate(const PagedAttendArgs& a, const
 }
 constexpr int kWholeStrip = 32 * kStrip;
 
-// A lane's share of a strip.
-template <int P> struct Frag {
-  static constexpr int G = P / 32;
-  uint32_t k[2][G];      // tokens lane / 4 and + 8: the words (lane % 4, g)
-  uint32_t v[2][G];      // halves 0 and 1: unit pairs (lane / 4, lane % 4, g)
-  uint32_t s[2][G];      // tokens lane / 4 and + 8: K scales, then V scales, two to a word
-};
-
-template <int P>
-__device__ __forceinline__ void load_frag(const uint8_t* strip, int lane, Frag<P>& f) {
-  constexpr int G = P / 32;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const uint8_t* kp = strip + half * 4 * P + lane * (G * 4);
-    const uint8_t* vp = strip + 8 * P + half * 4 * P + lane * (G * 4);
-    const uint8_t* sp = strip + 16 * P + (lane / 4 + 8 * half) * (G * 4);
-    if constexpr (G == 4) {
-      const uint4 a = *reinterpret_cast<const uint4*>(kp);
-      const uint4 b = *reinterpret_cast<const uint4*>(vp);
-      const uint4 c = *reinterpret_cast<const uint4*>(sp);
-      f.k[half][0] = a.x; f.k[half][1] = a.y; f.k[half][2] = a.z; f.k[half][3] = a.w;
-      f.v[half][0] = b.x; f.v[half][1] = b.y; f.v[half][2] = b.z; f.v[half][3] = b.w;
-      f.s[half][0] = c.x; f.s[half][1] = c.y; f.s[half][2] = c.z; f.s[half][3] = c.w;
-    } else {
-      const uint2 a = *reinterpret_cast<const uint2*>(kp);
-      const uint2 b = *reinterpret_cast<const uint2*>(vp);
-      const uint2 c = *reinterpret_cast<const uint2*>(sp);
-      f.k[half][0] = a.x; f.k[half][1] = a.y;
-      f.v[half][0] = b.x; f.v[half][1] = b.y;
-      f.s[half][0] = c.x; f.s[half][1] = c.y;
-    }
+// The G words of a lane at p.
+template <int G> __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
+  if constexpr (G == 4) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    w[0] = a.x; w[1] = a.y;
   }
 }
-template <int G>
-__device__ __forceinline__ float scale_of(const uint32_t* s, int i) {  // i-th of 2 G bf16 values
+__device__ __forceinline__ float bf16_of(const uint32_t* s, int i) {  // i-th of packed bf16 values
   const uint32_t w = s[i >> 1];
   return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // (a NaN gives way)
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // The q operand of a warp: for kWide with a lo part, hi then lo.
@@ -208,145 +197,167 @@ template <int P, bool kWide, bool kLo> struct QFrag {
 };
 
 // A warp's running state for the unit's heads; lane (t, c) = (lane / 4, lane % 4) holds head c
-// (packed) or heads 2 c and 2 c + 1 (wide).
+// (packed) or heads 2 c and 2 c + 1 (wide).  A weight is 2^(y - m), y the logit in log2 units;
+// the values' scales are taken times 2^e, which keeps weight x scale within a half's range.
 template <int P, bool kWide> struct State {
   static constexpr int HL = kWide ? 2 : 1, G = P / 32;
-  float m[HL], l[HL];   // reference (log2 units); this lane's part of the sum
-  float acc[2 * G][4];  // dims 32 g + 4 t + {0..3}: packed hi and lo columns, wide two heads
-  int e;                // V scales are multiplied by 2^e
+  float m[HL], l[HL];    // reference; this lane's part of the weights' sum
+  float top[HL];         // a logit above it moves the reference
+  float most;            // a scale above it moves e
+  float acc[2 * G][4];   // dims 32 g + 4 t + {0..3}: packed hi and lo columns, wide two heads
+  int e;
 };
 
 template <int P, bool kWide, bool kLo>
-__device__ __forceinline__ void strip_step(const Frag<P>& f, int valid,
-                                           const QFrag<P, kWide, kLo>& q, const float* fac,
-                                           State<P, kWide>& st) {
-  constexpr int G = P / 32, HL = kWide ? 2 : 1;
-  const int t = (threadIdx.x & 31) >> 2;
-  const bool whole = valid == kWholeStrip;
-  // logits of tokens t and t + 8 for the lane's heads
-  float x[HL][2];
+__device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int valid1,
+                                          const QFrag<P, kWide, kLo>& q, const float* fac,
+                                          State<P, kWide>& st) {
+  constexpr int G = P / 32, HL = kWide ? 2 : 1, SB = strip_bytes(P);
+  const int lane = threadIdx.x & 31, t = lane >> 2;
+  const bool whole = valid0 == kWholeStrip && valid1 == kWholeStrip;
+  float y[HL][2][2];        // logits of tokens t and t + 8 of each strip for the lane's heads
+  uint32_t sv[2][2][G / 2]; // their V scales, two to a word
 #pragma unroll
-  for (int i = 0; i < HL; ++i) x[i][0] = x[i][1] = 0.f;
+  for (int n = 0; n < 2; ++n) {
+    uint32_t k[2][G], sc[2][G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const uint32_t w0 = f.k[0][g], w1 = f.k[1][g], u0 = w0 >> 8, u1 = w1 >> 8;
-    const uint32_t a0[4] = {codes2<0>(w0), codes2<0>(w1), codes2<1>(w0), codes2<1>(w1)};
-    const uint32_t a1[4] = {codes2<0>(u0), codes2<0>(u1), codes2<1>(u0), codes2<1>(u1)};
-    const float s0 = scale_of<G>(f.s[0], g), s1 = scale_of<G>(f.s[1], g);
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int half = 0; half < 2; ++half) {
+      load_words<G>(strips + n * SB + half * 4 * P + lane * (G * 4), k[half]);
+      load_words<G>(strips + n * SB + 16 * P + (t + 8 * half) * (G * 4), sc[half]);
 #pragma unroll
-    for (int p = 0; p < QFrag<P, kWide, kLo>::kParts; ++p) {
-      mma16816(d, a0, &q.w[p][4 * g]);
-      mma16816(d, a1, &q.w[p][4 * g + 2]);
+      for (int i = 0; i < G / 2; ++i) sv[n][half][i] = sc[half][G / 2 + i];
     }
-    if constexpr (kWide) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[i][0] = fmaf(s0, d[i], x[i][0]);
-        x[i][1] = fmaf(s1, d[2 + i], x[i][1]);
-      }
-    } else {
-      x[0][0] = fmaf(s0, d[0] + d[1], x[0][0]);
-      x[0][1] = fmaf(s1, d[2] + d[3], x[0][1]);
-    }
-  }
-  float sv[2][G];
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    sv[0][g] = scale_of<G>(f.s[0], G + g);
-    sv[1][g] = scale_of<G>(f.s[1], G + g);
-  }
-  bool live0 = true, live1 = true;
-  if (!whole) {
-    const int ra = valid & 31, rb = valid >> 5;
-    live0 = t >= ra && t < rb;
-    live1 = t + 8 >= ra && t + 8 < rb;
+    for (int i = 0; i < HL; ++i) y[i][n][0] = y[i][n][1] = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      sv[0][g] = live0 ? sv[0][g] : 0.f;
-      sv[1][g] = live1 ? sv[1][g] : 0.f;
-    }
-  }
-  float smax = 0.f;
+      const uint32_t w0 = k[0][g], w1 = k[1][g], u0 = w0 >> 8, u1 = w1 >> 8;
+      const uint32_t a0[4] = {codes2<0>(w0), codes2<0>(w1), codes2<1>(w0), codes2<1>(w1)};
+      const uint32_t a1[4] = {codes2<0>(u0), codes2<0>(u1), codes2<1>(u0), codes2<1>(u1)};
+      float d[4];
 #pragma unroll
-  for (int g = 0; g < G; ++g) smax = fmaxf(smax, fmaxf(sv[0][g], sv[1][g]));
+      for (int p = 0; p < QFrag<P, kWide, kLo>::kParts; ++p) {
+        if (p == 0) mma16816_first(d, a0, &q.w[p][4 * g]);
+        else mma16816(d, a0, &q.w[p][4 * g]);
+        mma16816(d, a1, &q.w[p][4 * g + 2]);
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float s = bf16_of(sc[half], g);
+        if constexpr (kWide) {
+          y[0][n][half] = fmaf(s, d[2 * half], y[0][n][half]);
+          y[HL - 1][n][half] = fmaf(s, d[2 * half + 1], y[HL - 1][n][half]);
+        } else {
+          y[0][n][half] = fmaf(s, d[2 * half] + d[2 * half + 1], y[0][n][half]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < HL; ++i)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) y[i][n][half] *= fac[i];
+  }
+  if (!whole) {  // rows outside the attended set: no weight, and nothing of their scales
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int valid = n == 0 ? valid0 : valid1;
+        if (t + 8 * half >= (valid & 31) && t + 8 * half < (valid >> 5)) continue;
+#pragma unroll
+        for (int i = 0; i < G / 2; ++i) sv[n][half][i] = 0;
+#pragma unroll
+        for (int i = 0; i < HL; ++i) y[i][n][half] = -INFINITY;
+      }
+  }
   // the reference moves where a logit or a scale outgrows it
-  bool grow = smax * pow2(st.e) >= static_cast<float>(2 << kScaleTop);
+  uint32_t s2 = 0;
+#pragma unroll
+  for (int i = 0; i < 2 * 2 * (G / 2); ++i)
+    s2 = max_bf16x2(s2, sv[i / G][(i / (G / 2)) & 1][i % (G / 2)]);
+  float smax = fmaxf(bf16_of(&s2, 0), bf16_of(&s2, 1));
+  bool grow = smax > st.most;
+  float ymax[HL];
 #pragma unroll
   for (int i = 0; i < HL; ++i) {
-    x[i][0] = live0 ? x[i][0] * fac[i] : -INFINITY;
-    x[i][1] = live1 ? x[i][1] * fac[i] : -INFINITY;
-    grow |= fmaxf(x[i][0], x[i][1]) > st.m[i] + kSlack;
+    ymax[i] = fmaxf(fmaxf(y[i][0][0], y[i][0][1]), fmaxf(y[i][1][0], y[i][1][1]));
+    grow |= ymax[i] > st.top[i];
   }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
-    const int e = min(st.e, max(kScaleTop - 1 - exponent(smax), -120));
-    const float fe = e == st.e ? 1.f : pow2(max(e - st.e, -126));
+    const int e = min(st.e, max(kScaleTop - 1 - exponent(smax), kLeastE));
+    const float fe = pow2(max(e - st.e, -126));
     st.e = e;
-    float fm[HL];
+    st.most = pow2(kScaleTop - e);
+    float f[HL];
 #pragma unroll
     for (int i = 0; i < HL; ++i) {
-      float top = fmaxf(x[i][0], x[i][1]);
+      float m = ymax[i];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float m = fmaxf(st.m[i], top);
-      fm[i] = m == st.m[i] ? 1.f : ex2(st.m[i] - m);
+      for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = fmaxf(st.m[i], m);
+      f[i] = m == st.m[i] ? 1.f : ex2(st.m[i] - m);
       st.m[i] = m;
-      st.l[i] *= fm[i];
-      fm[i] *= fe;
+      st.top[i] = m + kSlack;
+      st.l[i] *= f[i];
+      f[i] *= fe;
     }
 #pragma unroll
     for (int b = 0; b < 2 * G; ++b)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) st.acc[b][j] *= fm[kWide ? (j & 1) : 0];
+      for (int j = 0; j < 4; ++j) st.acc[b][j] *= f[kWide ? (j & 1) : 0];
   }
   const float up = pow2(st.e);
 #pragma unroll
-  for (int i = 0; i < HL; ++i) {
-    float p0 = ex2(x[i][0] - st.m[i]), p1 = ex2(x[i][1] - st.m[i]);
-    if (!whole) {
-      p0 = live0 ? p0 : 0.f;
-      p1 = live1 ? p1 : 0.f;
-    }
-    st.l[i] += p0 + p1;
-    x[i][0] = p0 * up;
-    x[i][1] = p1 * up;
-  }
+  for (int i = 0; i < HL; ++i)
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    // codes of the group's two 16-dim tiles
-    uint32_t a0[4], a1[4];
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const uint32_t w = f.v[half][g], u = w >> 8;
-      a0[2 * half] = codes2<0>(w);
-      a0[2 * half + 1] = codes2<1>(w);
-      a1[2 * half] = codes2<0>(u);
-      a1[2 * half + 1] = codes2<1>(u);
-    }
-    // weights with the group's scale, hi + lo halves (11 + 11 bits)
-    float hi[HL][2], lo[HL][2];
-#pragma unroll
-    for (int i = 0; i < HL; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float w = x[i][j] * sv[j][g];
-        hi[i][j] = __uint_as_float(__float_as_uint(w) & 0xffffe000u);
-        lo[i][j] = w - hi[i][j];
+      for (int half = 0; half < 2; ++half) {
+        float p = ex2(y[i][n][half] - st.m[i]);
+        // (a row without weight before any row with one: -infinity against -infinity)
+        if (!whole) p = y[i][n][half] == -INFINITY ? 0.f : p;
+        st.l[i] += p;
+        y[i][n][half] = p * up;
       }
-    uint32_t b[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      b[j] = transpose8x8(kWide ? pack_half2(hi[0][j], hi[HL - 1][j])
-                                : pack_half2(hi[0][j], lo[0][j]));
-    mma16816(st.acc[2 * g], a0, b);
-    mma16816(st.acc[2 * g + 1], a1, b);
-    if constexpr (kWide) {
+  for (int n = 0; n < 2; ++n) {
+    uint32_t v[2][G];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) b[j] = transpose8x8(pack_half2(lo[0][j], lo[HL - 1][j]));
+    for (int half = 0; half < 2; ++half)
+      load_words<G>(strips + n * SB + 8 * P + half * 4 * P + lane * (G * 4), v[half]);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      // codes of the group's two 16-dim tiles
+      const uint32_t w0 = v[0][g], w1 = v[1][g], u0 = w0 >> 8, u1 = w1 >> 8;
+      const uint32_t a0[4] = {codes2<0>(w0), codes2<1>(w0), codes2<0>(w1), codes2<1>(w1)};
+      const uint32_t a1[4] = {codes2<0>(u0), codes2<1>(u0), codes2<0>(u1), codes2<1>(u1)};
+      // weights with the group's scale, hi + lo halves (11 + 11 bits)
+      float hi[HL][2], lo[HL][2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float s = bf16_of(sv[n][half], g);
+#pragma unroll
+        for (int i = 0; i < HL; ++i) {
+          const float w = y[i][n][half] * s;
+          hi[i][half] = __uint_as_float(__float_as_uint(w) & 0xffffe000u);
+          lo[i][half] = w - hi[i][half];
+        }
+      }
+      uint32_t b[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        b[j] = transpose8x8(kWide ? pack_half2(hi[0][j], hi[HL - 1][j])
+                                  : pack_half2(hi[0][j], lo[0][j]));
       mma16816(st.acc[2 * g], a0, b);
       mma16816(st.acc[2 * g + 1], a1, b);
+      if constexpr (kWide) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) b[j] = transpose8x8(pack_half2(lo[0][j], lo[HL - 1][j]));
+        mma16816(st.acc[2 * g], a0, b);
+        mma16816(st.acc[2 * g + 1], a1, b);
+      }
     }
   }
 }
@@ -357,7 +368,7 @@ template <int P, bool kWide, bool kLo> struct Smem {
   static constexpr int H = kWide ? 8 : 4;
   static constexpr int kRow = P + 4;            // out, then m and l
   static constexpr int kSlot = H * kRow;
-  static constexpr int kRing = kWarps * kStages * strip_bytes(P);
+  static constexpr int kRing = kWarps * kStages * 2 * strip_bytes(P);
   static constexpr int kSlots = kRing;
   static constexpr int kQ = kSlots + kWarps * kSlot * 4;
   static constexpr int kFac = kQ + QFrag<P, kWide, kLo>::kParts * (P / 8) * 32 * 4;
@@ -432,19 +443,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   __shared__ uint32_t s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = a.heads * a.chunks;  // per request
-  char* ring = sm + warp * kStages * SB;
+  char* ring = sm + warp * kStages * 2 * SB;
   uint16_t* info = reinterpret_cast<uint16_t*>(sm + S::kInfo) + warp * 64;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBars) + warp * kStages;
   if (lane < kStages) mbar_init(bars + lane, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (tid == 0) s_long = 0;
 
-  // strips before each request (of one unit), and the longest unit
+  // pairs of strips before each request (of one unit), and the longest unit
   int64_t run = 0;
   for (int base = 0; base < a.R; base += kThreads) {
     const int r = base + tid;
     int n = 0;
-    if (r < a.R) n = unit_map(a, paged_len(a.lens, r, a.bs, a.max_pages, a.status)).total();
+    if (r < a.R) n = (unit_map(a, paged_len(a.lens, r, a.bs, a.max_pages, a.status)).total() + 1) / 2;
     int64_t tot;
     const int64_t ex = block_scan64(n, s_w, &tot);  // (two barriers: s_long is set by now)
     if (r < a.R) pre[r] = static_cast<int32_t>(run + ex);
@@ -468,48 +480,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   if (first >= all) return;
   const uint32_t begin = static_cast<uint32_t>(first), end = min(all, begin + chunk);
 
-  // the warp's strips: begin + warp, + 8, ..
+  // the warp's pairs: begin + warp, + 8, ..
   const int mine = static_cast<int>(end - begin) > warp
                        ? static_cast<int>(end - begin - warp + kWarps - 1) / kWarps : 0;
-  const uint8_t* src = a.pool;  // of the lane's strip in the current round of 32
+  const uint8_t* src = a.pool;  // of the lane's strip in the current round of 16 pairs
   int valid = 0;
-  int dead_at = -1;             // the strip whose wait ran out: nothing is issued or awaited after
-  auto find = [&](int j0) {     // lane i finds strip j0 + i
+  unsigned some = 0;            // lanes whose strip has rows to attend to
+  int dead_at = -1;             // the pair whose wait ran out: nothing is issued or awaited after
+  auto find = [&](int j0) {     // lane i finds strip i % 2 of pair j0 + i / 2
     valid = 0;
-    const int j = j0 + lane;
+    const int j = j0 + lane / 2;
     if (j < mine) {
       const uint32_t at = begin + warp + uint32_t(j) * kWarps;
       const int r = last_at_most(pre, a.R, static_cast<int32_t>(at / units));
       const uint32_t n = pre[r + 1] - pre[r], in = at - uint32_t(pre[r]) * units, u = in / n;
-      src = locate(a, unit_map(a, a.lens[r]), r, static_cast<int>(u) / a.chunks,
-                   static_cast<int>(in - u * n), SB, &valid);
+      const int v = 2 * static_cast<int>(in - u * n) + (lane & 1);
+      const UnitMap map = unit_map(a, a.lens[r]);
+      if (v < map.total())
+        src = locate(a, map, r, static_cast<int>(u) / a.chunks, v, SB, &valid);
     }
-    info[(j0 + lane) & 63] = static_cast<uint16_t>(valid);
+    some = __ballot_sync(0xffffffffu, valid != 0);
+    info[(2 * j0 + lane) & 63] = static_cast<uint16_t>(valid);
     __syncwarp();
   };
-  auto issue = [&](int j) {  // strip j into its stage (which is free), by the lane that found it
+  auto issue = [&](int j) {  // pair j into its stage (which is free), by the lanes that found it
     if (j >= mine) return;
-    if ((j & 31) == 0) find(j);
-    if (lane == (j & 31)) {
+    if ((j & 15) == 0) find(j);
+    if (lane / 2 == (j & 15)) {
       uint64_t* bar = bars + j % kStages;
-      if (valid != 0) {
-        mbar_arrive_tx(bar, SB);
-        bulk_g2s(ring + (j % kStages) * SB, src, SB, bar);
-      } else {
-        mbar_arrive(bar);
-      }
+      if ((lane & 1) == 0) mbar_arrive_tx(bar, SB * __popc((some >> lane) & 3u));
+      if (valid != 0)
+        bulk_g2s(ring + ((j % kStages) * 2 + (lane & 1)) * SB, src, SB, bar);
     }
   };
 #pragma unroll 1
   for (int j = 0; j < kStages; ++j) issue(j);
 
-  int j = 0;  // the warp's next strip
+  int j = 0;  // the warp's next pair
   for (uint32_t at = begin; at < end;) {
     const int r = last_at_most(pre, a.R, static_cast<int32_t>(at / units));
     const uint32_t n = pre[r + 1] - pre[r], base = uint32_t(pre[r]) * units;
     const uint32_t u = (at - base) / n;
     const int h = static_cast<int>(u) / a.chunks, h0 = (static_cast<int>(u) - h * a.chunks) * H;
-    const uint32_t u0 = base + u * n;             // the unit's first strip
+    const uint32_t u0 = base + u * n;             // the unit's first pair
     const uint32_t stop = min(end, u0 + n);
     const int nh = min(H, a.group - h0);
     {
@@ -531,11 +544,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       }
     float fac[HL];
     State<P, kWide> st;
-    st.e = 120;
+    st.e = kMostE;
+    st.most = pow2(kScaleTop - kMostE);
 #pragma unroll
     for (int i = 0; i < HL; ++i) {
       fac[i] = s_fac[HL * (lane & 3) + i];
-      st.m[i] = -INFINITY;
+      st.m[i] = st.top[i] = -INFINITY;
       st.l[i] = 0.f;
     }
 #pragma unroll
@@ -561,12 +575,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
           continue;
         }
       }
-      const int v = info[j & 63];
-      Frag<P> f;
-      if (v != 0) load_frag<P>(reinterpret_cast<const uint8_t*>(ring + stage * SB), lane, f);
+      const int v0 = info[(2 * j) & 63], v1 = info[(2 * j + 1) & 63];
+      if (v0 | v1)
+        pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + stage * 2 * SB), v0, v1,
+                                 qf, fac, st);
       __syncwarp();
       issue(j + kStages);
-      if (v != 0) strip_step<P, kWide, kLo>(f, v, qf, fac, st);
     }
 
     // warp states to shared memory
@@ -630,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       }
     }
     if (!whole) {
-      // the unit's CTAs: i0 holds its first strip, i1 its last
+      // the unit's CTAs: i0 holds its first pair, i1 its last
       const int i0 = u0 / chunk, i1 = (u0 + n - 1) / chunk;
       __threadfence();
       __syncthreads();
