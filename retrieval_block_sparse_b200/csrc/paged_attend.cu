@@ -656,26 +656,67 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       __syncthreads();
       if (s_last) {
         __threadfence();
-        // i0's part is its second one unless its range starts with the unit
+        // Warps take rows and shares of the parts, eight parts' loads in flight; the shares meet
+        // in shared memory.  (i0's part is its second one unless its range starts the unit.)
         const float* p0 = a.parts + (int64_t(i0) * 2 + (uint64_t(chunk) * i0 >= u0 ? 0 : 1)) * S::kSlot;
         const float* p1 = a.parts + int64_t(i0) * 2 * S::kSlot;
-        for (int i = tid; i < nh * P; i += kThreads) {
-          const int hh = i / P, d = i % P;
-          const int off = hh * S::kRow;
-          float m = __ldcg(p0 + off + P);
-#pragma unroll 8
-          for (int c = 1; c <= i1 - i0; ++c)
-            m = fmaxf(m, __ldcg(p1 + int64_t(c) * 2 * S::kSlot + off + P));
-          float l = 0.f, o = 0.f;
-#pragma unroll 8
-          for (int c = 0; c <= i1 - i0; ++c) {
-            const float* s = (c == 0 ? p0 : p1 + int64_t(c) * 2 * S::kSlot) + off;
-            const float pm = __ldcg(s + P), pl = __ldcg(s + P + 1), po = __ldcg(s + d);
-            const float f = pm == m ? 1.f : ex2(pm - m);
-            l += f * pl;
-            o += f * po;
+        constexpr int kShares = kWarps / H;
+        const int hh = warp % H, share = warp / H, np = i1 - i0 + 1;
+        if (hh < nh) {
+          float m = -INFINITY, l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          constexpr int kU = 8;
+          for (int c0 = share; c0 < np; c0 += kU * kShares) {
+            float pm[kU], pl[kU];
+            float4 po[kU];
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+              const int c = c0 + i * kShares;
+              pm[i] = -INFINITY;
+              pl[i] = 0.f;
+              po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (c < np) {
+                const float* s = (c == 0 ? p0 : p1 + int64_t(c) * 2 * S::kSlot) + hh * S::kRow;
+                pm[i] = __ldcg(s + P);
+                pl[i] = __ldcg(s + P + 1);
+                if (lane * 4 < P) po[i] = __ldcg(reinterpret_cast<const float4*>(s) + lane);
+              }
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kU; ++i) top = fmaxf(top, pm[i]);
+            const float f0 = m == top ? 1.f : ex2(m - top);
+            l *= f0;
+            o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+            m = top;
+#pragma unroll
+            for (int i = 0; i < kU; ++i) {
+              const float f = pm[i] == top ? 1.f : ex2(pm[i] - top);
+              l += f * pl[i];
+              o.x += f * po[i].x; o.y += f * po[i].y; o.z += f * po[i].z; o.w += f * po[i].w;
+            }
           }
-          finish(a, row0 + hh, d, m, l, o);
+          float* s = slots + (share * H + hh) * S::kRow;
+          if (lane * 4 < P) *reinterpret_cast<float4*>(s + lane * 4) = o;
+          if (lane == 0) {
+            s[P] = m;
+            s[P + 1] = l;
+          }
+        }
+        __syncthreads();
+        for (int i = tid; i < nh * P; i += kThreads) {
+          const int row = i / P, d = i % P;
+          const float* s = slots + row * S::kRow;
+          float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+          for (int w = 0; w < kShares; ++w) m = fmaxf(m, s[w * S::kSlot + P]);
+#pragma unroll
+          for (int w = 0; w < kShares; ++w) {
+            const float f = s[w * S::kSlot + P] == m ? 1.f : ex2(s[w * S::kSlot + P] - m);
+            l += f * s[w * S::kSlot + P + 1];
+            o += f * s[w * S::kSlot + d];
+          }
+          finish(a, row0 + row, d, m, l, o);
         }
       }
     }
