@@ -541,6 +541,9 @@ class PagedStore:
         self.n_free = buf("n_free", n_free, (1,), torch.int32,
                           lambda s, dt: torch.full(s, n_pages, dtype=dt, device=dev))
         self.device = self.pool.device
+        if not self.pool.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        self._index, self._td = self.device.index, _tdtype(self.dtype)
         self.status = zeros((8,), torch.int32)
         d = _PagedDesc(n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
                        max_pages, self.dtype)
@@ -562,12 +565,12 @@ class PagedStore:
     def tdtype(self):
         return _tdtype(self.dtype)
 
-    # -- marshalling -----------------------------------------------------------
+    # -- marshalling (a decode step makes four calls: host time counts) ----------
     def _call(self, name, *args):
         """One library call on the store's device and torch's current stream there."""
-        i = self.device.index
-        stream = torch.cuda.current_stream(i).cuda_stream
-        if torch.cuda.current_device() == i:
+        i = self._index
+        stream = torch._C._cuda_getCurrentRawStream(i)
+        if torch._C._cuda_getDevice() == i:
             s = getattr(_LIB, name)(self.handle, *args, stream)
         else:
             with torch.cuda.device(i):
@@ -575,25 +578,34 @@ class PagedStore:
         if s != OK:
             raise RbaError(s, name)
 
+    def _refuse(self, name, t, shape, dt):
+        raise ValueError(f"{name}: expected a {dt} tensor {shape} on {self.device} with dense "
+                         f"dims, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}, on "
+                         f"{t.device}")
+
     def _arg(self, name, t, shape, dt):
         """Pointer of a contiguous tensor of exactly this shape, type and device."""
-        if t.dtype != dt or tuple(t.shape) != shape or t.device != self.device:
-            raise ValueError(f"{name}: expected {dt} {shape} on {self.device}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
+        if t.dtype is not dt or t.shape != shape or t.get_device() != self._index or \
+                not t.is_contiguous():
+            self._refuse(name, t, shape, dt)
         return t.data_ptr()
 
     def _rows(self, name, t, n, heads):
         """(pointer, row stride, head stride) of rows [n][heads][D] with dense dims."""
-        if t.dtype != self.tdtype or tuple(t.shape) != (n, heads, self.D) or \
-                t.device != self.device:
-            raise ValueError(f"{name}: expected {self.tdtype} {(n, heads, self.D)} on "
-                             f"{self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        sn, sh, sd = t.stride()
-        if sd != 1 and self.D > 1:
-            raise ValueError(f"{name}: the head dim must be dense")
+        sn, sh, sd = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if t.dtype is not self._td or t.shape != (n, heads, self.D) or sd != 1 or \
+                t.get_device() != self._index:
+            self._refuse(name, t, (n, heads, self.D), self._td)
         return t.data_ptr(), sn, sh
+
+    def _bytes(self, t):
+        """(pointer, bytes) of a workspace."""
+        if t.dtype is not torch.uint8 or t.get_device() != self._index or not t.is_contiguous():
+            self._refuse("workspace", t, tuple(t.shape), torch.uint8)
+        return t.data_ptr(), t.numel()
+
+    def _new(self, shape, dt):
+        return torch.empty(shape, dtype=dt, device=self.device)
 
     # -- page tables -------------------------------------------------------------
     def extend(self, n_new, n_slots, *, slots=None, starts=None):
@@ -601,9 +613,9 @@ class PagedStore:
         tokens; starts [R + 1], the first new token of each request)."""
         R = n_new.shape[0]
         if slots is None:
-            slots = torch.empty(n_slots, dtype=torch.int32, device=self.device)
+            slots = self._new((n_slots,), torch.int32)
         if starts is None:
-            starts = torch.empty(R + 1, dtype=torch.int32, device=self.device)
+            starts = self._new((R + 1,), torch.int32)
         self._call("rba_paged_extend", self._arg("n_new", n_new, (R,), torch.int32), R,
                    self._arg("slots", slots, (n_slots,), torch.int32), n_slots,
                    self._arg("starts", starts, (R + 1,), torch.int32))
@@ -629,11 +641,11 @@ class PagedStore:
         n = slots.shape[0]
         shape = (n, self.Hkv, self.D)
         if k is None:
-            k = torch.empty(shape, dtype=self.tdtype, device=self.device)
+            k = self._new(shape, self._td)
         if v is None:
-            v = torch.empty(shape, dtype=self.tdtype, device=self.device)
+            v = self._new(shape, self._td)
         self._call("rba_paged_read", self._arg("slots", slots, (n,), torch.int32), n,
-                   self._arg("k", k, shape, self.tdtype), self._arg("v", v, shape, self.tdtype))
+                   self._arg("k", k, shape, self._td), self._arg("v", v, shape, self._td))
         return k, v
 
     # -- select, attend --------------------------------------------------------------
@@ -647,12 +659,11 @@ class PagedStore:
         R = q.shape[0]
         qp, qr, qh = self._rows("q", q, R, self.Hq)
         if idx is None:
-            idx = torch.empty((R, self.Hkv, k), dtype=torch.int32, device=self.device)
+            idx = self._new((R, self.Hkv, k), torch.int32)
         if workspace is None:
             workspace = self.select_workspace()
         self._call("rba_paged_select", qp, qr, qh, R, k, sink, window,
-                   self._arg("idx", idx, (R, self.Hkv, k), torch.int32), workspace.data_ptr(),
-                   workspace.numel())
+                   self._arg("idx", idx, (R, self.Hkv, k), torch.int32), *self._bytes(workspace))
         return idx
 
     def attend_workspace(self):
@@ -671,15 +682,14 @@ class PagedStore:
         if scale is None:
             scale = 1.0 / math.sqrt(self.D)
         if out is None:
-            out = torch.empty((R, self.Hq, self.D), dtype=torch.float32, device=self.device)
+            out = self._new((R, self.Hq, self.D), torch.float32)
         if lse is None:
-            lse = torch.empty((R, self.Hq), dtype=torch.float32, device=self.device)
+            lse = self._new((R, self.Hq), torch.float32)
         if workspace is None:
             workspace = self.attend_workspace()
         self._call("rba_paged_attend", qp, qr, qh, R, ip, k, sink, window, scale,
                    self._arg("out", out, (R, self.Hq, self.D), torch.float32),
-                   self._arg("lse", lse, (R, self.Hq), torch.float32), workspace.data_ptr(),
-                   workspace.numel())
+                   self._arg("lse", lse, (R, self.Hq), torch.float32), *self._bytes(workspace))
         return out, lse
 
     def check(self):
