@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kTableThreads) extend_kernel(TableArgs a) {
   __shared__ int32_t s_start[kMaxRequests + 1], s_page[kMaxRequests + 1];
   __shared__ int64_t s_w[32];
   __shared__ int s_last;
+  wait_for_stream();
   const int tid = threadIdx.x, R = a.n_requests;
   int len[kPer], add[kPer];
   int64_t tok = 0, pag = 0;
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(kTableThreads) truncate_kernel(TableArgs a) {
   __shared__ int32_t s_page[kMaxRequests + 1];
   __shared__ int64_t s_w[32];
   __shared__ int s_last;
+  wait_for_stream();
   const int tid = threadIdx.x, R = a.n_requests;
   int kept[kPer], freed[kPer];
   int64_t pag = 0;
@@ -254,8 +256,7 @@ rba_status rba_paged_extend(rba_paged* s, const int32_t* n_new, int32_t n_reques
   a.starts = starts;
   int grid = (n_slots + kTableThreads - 1) / kTableThreads;
   grid = grid < 1 ? 1 : grid > num_sms() ? num_sms() : grid;
-  extend_kernel<<<grid, kTableThreads, 0, stream>>>(a);
-  RBA_LAUNCH_CHECK();
+  RBA_CUDA_TRY(launch_dependent(extend_kernel, static_cast<unsigned>(grid), kTableThreads, 0, stream, a));
   return RBA_OK;
 }
 
@@ -268,8 +269,7 @@ rba_status rba_paged_truncate(rba_paged* s, const int32_t* keep, int32_t n_reque
   // at most a store's pages come back
   int grid = (s->d.n_pages + 4 * kTableThreads - 1) / (4 * kTableThreads);
   grid = grid > num_sms() ? num_sms() : grid;
-  truncate_kernel<<<grid, kTableThreads, 0, stream>>>(a);
-  RBA_LAUNCH_CHECK();
+  RBA_CUDA_TRY(launch_dependent(truncate_kernel, static_cast<unsigned>(grid), kTableThreads, 0, stream, a));
   return RBA_OK;
 }
 

@@ -106,6 +106,31 @@ __device__ __forceinline__ int last_at_most(const T* pre, int n, T x) {
   return lo;
 }
 
+// Every paged kernel is launched as a programmatic dependent of the one before it on the stream:
+// its CTAs come up while that one runs and wait here, before their first access to memory, until
+// it has completed.
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... A>
+cudaError_t launch_dependent(void (*kernel)(A...), unsigned grid, int threads, size_t smem,
+                             cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 // Top k per row of scores [rows][row_stride], row = request * heads + kv head: the request's
 // candidates only, written as page numbers ascending, then -1.
 rba_status launch_topk_paged(const float* scores, int row_stride, int rows, int heads,

@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   if (tid == 0) s_long = 0;
+  wait_for_stream();
 
   // pairs of strips before each request (of one unit), and the longest unit
   int64_t run = 0;
@@ -742,10 +743,10 @@ size_t ticket_bytes(const rba_paged* s) {
 template <int P, bool kWide, typename T>
 rba_status launch(const PagedAttendArgs& a, cudaStream_t stream) {
   const size_t smem = Smem<P, kWide, sizeof(T) == 4>::bytes(a.R);
-  const auto kernel = paged_attend_kernel<P, kWide, T>;
+  void (*const kernel)(PagedAttendArgs) = paged_attend_kernel<P, kWide, T>;
   RBA_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kernel), smem));
-  kernel<<<num_sms() * kCtasPerSm, kThreads, smem, stream>>>(a);
-  RBA_LAUNCH_CHECK();
+  RBA_CUDA_TRY(launch_dependent(kernel, static_cast<unsigned>(num_sms() * kCtasPerSm), kThreads,
+                                smem, stream, a));
   return RBA_OK;
 }
 

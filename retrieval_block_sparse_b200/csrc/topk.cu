@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kRowThreads) topk_rows_kernel(const float* __r
 __global__ void __launch_bounds__(kRowThreads) topk_paged_rows_kernel(
     const float* __restrict__ scores, int row_stride, int heads, const int32_t* __restrict__ lens,
     int bs, int max_pages, int sink, int window, int k, int32_t* __restrict__ idx) {
+  wait_for_stream();
   extern __shared__ __align__(16) char sm[];
   float* vals = reinterpret_cast<float*>(sm);                               // [row_stride]
   uint8_t* flag = reinterpret_cast<uint8_t*>(sm + size_t(row_stride) * 4);  // [row_stride]
@@ -309,9 +310,9 @@ rba_status launch_topk_paged(const float* scores, int row_stride, int rows, int 
                              int k, int32_t* idx, cudaStream_t stream) {
   const size_t smem = size_t(row_stride) * 5 + 16;
   RBA_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(topk_paged_rows_kernel), smem));
-  topk_paged_rows_kernel<<<rows, kRowThreads, smem, stream>>>(
-      scores, row_stride, heads, lens, bs, max_pages, sink, window, k, idx);
-  RBA_LAUNCH_CHECK();
+  RBA_CUDA_TRY(launch_dependent(topk_paged_rows_kernel, static_cast<unsigned>(rows), kRowThreads,
+                                smem, stream, scores, row_stride, heads, lens, bs, max_pages, sink,
+                                window, k, idx));
   return RBA_OK;
 }
 
