@@ -594,10 +594,10 @@ size_t rba_paged_select_workspace_size(const rba_paged* store);
  *        entry that is no candidate is skipped and flagged.  k = 0 with a window of at least
  *        every length attends to all tokens.
  *   out  device fp32 [n_requests][Hq][D];  lse device fp32 [n_requests][Hq] or NULL
- *   workspace >= rba_paged_attend_workspace_size(), 16-byte aligned, zeroed before the first
- *        call (every call leaves its synchronisation words zero)
- * Errors: INVALID_ARG, UNSUPPORTED (n_requests * (max_pages + 2) * strips of a page * Hkv *
- * ceil(group / 8) above 2^31 - 1), WORKSPACE, CUDA. */
+ *   workspace >= rba_paged_attend_workspace_size(), 16-byte aligned (no contents are kept in it)
+ * Errors: INVALID_ARG, UNSUPPORTED (n_requests * Hkv * ceil(group / 8) units of up to
+ * ceil((max_pages + 2) * strips of a page / 2) + 8 each are more than 2^31 - 1 in all, or more than
+ * 2^31 - 1 rows of q), WORKSPACE, CUDA. */
 rba_status rba_paged_attend(const rba_paged* store, const void* q, int64_t q_request_stride,
                             int64_t q_head_stride, int32_t n_requests, const int32_t* idx,
                             int32_t k, int32_t sink, int32_t window, float scale, float* out,

@@ -40,23 +40,50 @@ template <int P> __device__ __forceinline__ int scale_at(int t, int which, int g
   return 16 * P + (t * 2 * (P / 32) + which * (P / 32) + g) * 2;
 }
 
+// x / d for 0 <= x < 2^31: with L = ceil(log2 d) and m = ceil(2^(31 + L) / d) (below 2^32 for
+// d > 1), m d - 2^(31 + L) < d <= 2^L, so (x m) >> (31 + L) is the quotient.
+struct FastDiv {
+  uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f = {d, 0, 0};
+  if (d <= 1) return f;
+  uint32_t L = 0;
+  while ((uint64_t(1) << L) < d) ++L;
+  f.m = static_cast<uint32_t>(((uint64_t(1) << (31 + L)) + d - 1) / d);
+  f.s = L - 1;
+  return f;
+}
+__device__ __forceinline__ int div(int x, const FastDiv& f) {
+  return f.d <= 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), f.m) >> f.s);
+}
+
 // One request's attended set, in strips.  Page j is a candidate when it is full and
 // meets [sink, w0); the window always covers the partial last page.
 struct PagedGeo {
   int T, w0, sink_end, first, nc;
 };
-__host__ __device__ inline PagedGeo paged_geo(int T, int bs, int sink, int window) {
+__host__ __device__ inline PagedGeo paged_geo(int T, int full, int w0_page, int first, int bs,
+                                              int sink, int window) {
+  // full = T / bs, w0_page = w0 / bs, first = sink / bs
   PagedGeo g;
-  const int full = T / bs;
   const int open = T > window ? T - window : 0;
   g.T = T;
   g.w0 = open < full * bs ? open : full * bs;
   g.sink_end = sink < g.w0 ? sink : g.w0;
-  g.first = sink / bs;
-  int hi = g.w0 / bs + (g.w0 % bs != 0);
+  g.first = first;
+  int hi = w0_page + (g.w0 > w0_page * bs);
   hi = hi < full ? hi : full;
-  g.nc = hi > g.first ? hi - g.first : 0;
+  g.nc = hi > first ? hi - first : 0;
   return g;
+}
+__host__ __device__ inline int paged_w0(int T, int full, int bs, int window) {
+  const int open = T > window ? T - window : 0;
+  return open < full * bs ? open : full * bs;
+}
+__host__ __device__ inline PagedGeo paged_geo(int T, int bs, int sink, int window) {
+  const int full = T / bs;
+  return paged_geo(T, full, paged_w0(T, full, bs, window) / bs, sink / bs, bs, sink, window);
 }
 
 // A request's length as the store holds it; a length outside the table is reported and

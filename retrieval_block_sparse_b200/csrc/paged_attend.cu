@@ -23,12 +23,19 @@
 // The running maximum is lazy: weights are taken relative to a reference that moves only when
 // a logit passes it by 2^4, so most strips need no cross-lane maximum and no rescale.
 //
-// Work.  All pairs of strips of all (request, kv head) units form one line, cut evenly over the
-// CTAs whatever the requests' lengths; warps take a CTA's pairs in turn, each through its own ring
-// of bulk copies, which runs on across units.  A CTA's part of a unit that it does not hold
-// whole goes to the workspace, and the last of the unit's CTAs to arrive merges the parts in
-// order.
+// Work.  All pairs of strips of all (request, kv head) units form one line, cut evenly over
+// workers whatever the requests' lengths, each unit counted with a few pairs more for what its
+// start and end cost.  A worker is a CTA, whose warps take its pairs in turn, or, where units are
+// short (a batch of short contexts, many kv heads), a single warp, which meets no barrier.  Each
+// warp has its own ring of bulk copies, which runs on across units.  (Taking the next pair
+// whenever there is room would even out the warps, but the sums' order, and with it the result,
+// would change from run to run.)  A worker's part of a unit that it does not hold whole goes to
+// the workspace, and a second kernel merges each unit's parts in order: cheaper than a ticket, a
+// fence and a merge by the last worker to arrive, which few warps would then wait for.  Where no
+// unit can be longer than kWholePairs, warps take whole units and there is no second kernel.
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "decode_persist.cuh"
 #include "paged.cuh"
@@ -36,11 +43,17 @@
 namespace rba {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 2;           // pairs of strips in a warp's ring
-constexpr int kLeast = kWarps;       // pairs a CTA takes at least (or a whole unit)
+constexpr int kStages = 2;  // pairs of strips in a warp's ring
+// What a unit's start and end cost, in pairs of its worker, and the pairs that a worker takes at
+// least (or a whole unit): for CTAs and for single warps.
+constexpr int kTeamCost = 8, kAloneCost = 2;
+constexpr int kTeamLeast = kWarps, kAloneLeast = 2;
+// Warps work alone where the longest unit is then cut into at most this many parts.
+constexpr int kAloneParts = 24;
+constexpr int kWholePairs = 8;
 constexpr float kToLog2 = 1.4426950408889634f;
 constexpr float kToLn = 0.6931471805599453f;
 constexpr float kSlack = 4.f;        // a logit may pass the reference by 2^4
@@ -57,11 +70,14 @@ struct PagedAttendArgs {
   int32_t* status;
   float* out;
   float* lse;
-  uint32_t* tickets;  // one per unit, zero between calls
-  float* parts;       // [CTA][2][heads of a unit][P + 4]
+  int2* units;        // per unit: its first part, and how many there are (1: nothing to merge)
+  float* parts;       // [worker][2][heads of a unit][P + 4]
   float scale;
   int R, heads, group, dim, bs, strips, max_pages, n_pages, k, sink, window;
   int chunks;         // head chunks of a kv head
+  int first;          // sink / bs
+  int whole;          // warps take whole units
+  FastDiv by_bs, by_strips, by_units, by_chunks;
 };
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -116,36 +132,37 @@ struct UnitMap {
   int ns, nk, nw, w_lin;  // strips of sink, of the selected pages, of the window; its first
   __device__ __forceinline__ int total() const { return ns + nk + nw; }
 };
-__device__ __forceinline__ int lin_strip(int pos, int bs, int strips) {
-  const int j = pos / bs;
-  return j * strips + (pos - j * bs) / kStrip;
-}
 __device__ __forceinline__ UnitMap unit_map(const PagedAttendArgs& a, int T) {
   UnitMap m;
-  m.g = paged_geo(T, a.bs, a.sink, a.window);
-  m.ns = m.g.sink_end > 0 ? lin_strip(m.g.sink_end - 1, a.bs, a.strips) + 1 : 0;
+  const int full = div(T, a.by_bs);
+  const int w0 = paged_w0(T, full, a.bs, a.window), w0_page = div(w0, a.by_bs);
+  m.g = paged_geo(T, full, w0_page, a.first, a.bs, a.sink, a.window);
+  const auto lin = [&](int pos, int page) {
+    return page * a.strips + (pos - page * a.bs) / kStrip;
+  };
+  m.ns = m.g.sink_end > 0 ? lin(m.g.sink_end - 1, div(m.g.sink_end - 1, a.by_bs)) + 1 : 0;
   m.nk = (a.k < m.g.nc ? a.k : m.g.nc) * a.strips;
-  m.w_lin = lin_strip(m.g.w0, a.bs, a.strips);
-  m.nw = T > m.g.w0 ? lin_strip(T - 1, a.bs, a.strips) - m.w_lin + 1 : 0;
+  m.w_lin = lin(w0, w0_page);
+  m.nw = T > w0 ? lin(T - 1, div(T - 1, a.by_bs)) - m.w_lin + 1 : 0;
   return m;
 }
 
-// Strip v of a unit: its address, and its valid rows [ra, rb) as ra + 32 rb (0 where nothing is
-// attended).
-__device__ __forceinline__ const uint8_t* locate(const PagedAttendArgs& a, const UnitMap& m, int r,
-                                                 int h, int v, int sbytes, int* valid) {
-  *valid = 0;
+// Strip v of a unit as a table entry: its byte offset in the pool, and its valid rows [ra, rb) as
+// (ra + 32 rb) << 48 (0: nothing of it is attended to).
+constexpr int kWholeStrip = 32 * kStrip;
+__device__ __forceinline__ uint64_t locate(const PagedAttendArgs& a, const UnitMap& m, int r,
+                                           int h, int v, int sbytes) {
   int lin, lo, hi;
   if (v < m.ns) {
     lin = v;
     lo = 0;
     hi = m.g.sink_end;
   } else if (v < m.ns + m.nk) {
-    const int i = (v - m.ns) / a.strips;
+    const int i = div(v - m.ns, a.by_strips);
     const int j = a.idx[(int64_t(r) * a.heads + h) * a.k + i];
     if (j < m.g.first || j >= m.g.first + m.g.nc) {
       report(a.status, RBA_ERR_BOUNDS, kWherePaged, j);
-      return a.pool;
+      return 0;
     }
     lin = j * a.strips + (v - m.ns) - i * a.strips;
     lo = m.g.sink_end;
@@ -155,19 +172,19 @@ __device__ __forceinline__ const uint8_t* locate(const PagedAttendArgs& a, const
     lo = m.g.w0;
     hi = m.g.T;
   }
-  const int j = lin / a.strips, sp = lin - j * a.strips;
+  const int j = div(lin, a.by_strips), sp = lin - j * a.strips;
   const int page = a.table[int64_t(r) * a.max_pages + j];
   if (page < 0 || page >= a.n_pages) {
     report(a.status, RBA_ERR_BOUNDS, kWherePaged, page);
-    return a.pool;
+    return 0;
   }
   const int pos0 = j * a.bs + sp * kStrip;
   const int ra = max(lo - pos0, 0);
   const int rb = min(min(kStrip, hi - pos0), a.bs - sp * kStrip);
-  if (rb > ra) *valid = ra + 32 * rb;
-  return a.pool + ((int64_t(page) * a.heads + h) * a.strips + sp) * sbytes;
+  if (rb <= ra) return 0;
+  return uint64_t((int64_t(page) * a.heads + h) * a.strips + sp) * sbytes |
+         uint64_t(ra + 32 * rb) << 48;
 }
-constexpr int kWholeStrip = 32 * kStrip;
 
 // The G words of a lane at p.
 template <int G> __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -189,12 +206,8 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // (a 
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// The q operand of a warp: for kWide with a lo part, hi then lo.
-template <int P, bool kWide, bool kLo> struct QFrag {
-  static constexpr int kParts = kWide && kLo ? 2 : 1;
-  static constexpr int kWords = P / 8;  // 32-bit words a lane holds of one part
-  uint32_t w[kParts][kWords];
-};
+// Parts of the q operand (in shared memory, read group by group): hi, and for wide 32-bit q lo.
+template <bool kWide, bool kLo> constexpr int q_parts() { return kWide && kLo ? 2 : 1; }
 
 // A warp's running state for the unit's heads; lane (t, c) = (lane / 4, lane % 4) holds head c
 // (packed) or heads 2 c and 2 c + 1 (wide).  A weight is 2^(y - m), y the logit in log2 units;
@@ -210,7 +223,7 @@ template <int P, bool kWide> struct State {
 
 template <int P, bool kWide, bool kLo>
 __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int valid1,
-                                          const QFrag<P, kWide, kLo>& q, const float* fac,
+                                          const uint32_t* qw, const float* fac,
                                           State<P, kWide>& st) {
   constexpr int G = P / 32, HL = kWide ? 2 : 1, SB = strip_bytes(P);
   const int lane = threadIdx.x & 31, t = lane >> 2;
@@ -236,10 +249,12 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
       const uint32_t a1[4] = {codes2<0>(u0), codes2<0>(u1), codes2<1>(u0), codes2<1>(u1)};
       float d[4];
 #pragma unroll
-      for (int p = 0; p < QFrag<P, kWide, kLo>::kParts; ++p) {
-        if (p == 0) mma16816_first(d, a0, &q.w[p][4 * g]);
-        else mma16816(d, a0, &q.w[p][4 * g]);
-        mma16816(d, a1, &q.w[p][4 * g + 2]);
+      for (int p = 0; p < q_parts<kWide, kLo>(); ++p) {
+        uint32_t q[4];
+        load_words<4>(reinterpret_cast<const uint8_t*>(qw + ((p * G + g) * 32 + lane) * 4), q);
+        if (p == 0) mma16816_first(d, a0, q);
+        else mma16816(d, a0, q);
+        mma16816(d, a1, q + 2);
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -362,37 +377,42 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
   }
 }
 
-// Shared memory: rings | warp states | q operand | factors | strips' valid rows | barriers |
-// strips before each request.
+// Shared memory: rings | warp states (warps working alone: their q operands) | q operand |
+// factors | where strips lie | barriers | pairs and units before each request.
 template <int P, bool kWide, bool kLo> struct Smem {
   static constexpr int H = kWide ? 8 : 4;
   static constexpr int kRow = P + 4;            // out, then m and l
   static constexpr int kSlot = H * kRow;
+  static constexpr int kQBytes = q_parts<kWide, kLo>() * (P / 8) * 32 * 4;
   static constexpr int kRing = kWarps * kStages * 2 * strip_bytes(P);
   static constexpr int kSlots = kRing;
   static constexpr int kQ = kSlots + kWarps * kSlot * 4;
-  static constexpr int kFac = kQ + QFrag<P, kWide, kLo>::kParts * (P / 8) * 32 * 4;
-  static constexpr int kInfo = kFac + 32;
-  static constexpr int kBars = kInfo + kWarps * 64 * 2;
+  static constexpr int kFac = kQ + kQBytes;
+  static constexpr int kWhere = kFac + kWarps * 32;
+  static constexpr int kBars = kWhere + kWarps * 64 * 8;
   static constexpr int kPre = kBars + kWarps * kStages * 8;
-  static size_t bytes(int R) { return kPre + size_t(R + 1) * 4; }
+  static_assert(kQBytes <= kSlot * 4, "a warp's q operand fits its state's place");
+  static size_t bytes(int R) { return kPre + size_t(R + 1) * 6; }
 };
 
-// q of the unit's heads into the products' B operand: warp `hh` takes head hh, scaled by a power
+// q of the unit's heads into the products' B operand: a warp takes head hh, scaled by a power
 // of two to a largest value in [2^14, 2^15), split hi + lo.  Word (part, 4 g + 2 ks + b) of lane
 // (t, c) holds dims 32 g + 8 c + 2 ks + b and that + 4 of column t.
-template <int P, bool kWide, bool kLo, typename T>
-__device__ __forceinline__ void stage_q(const PagedAttendArgs& a, const T* q, bool live,
-                                        uint32_t* qw, float* fac) {
-  using S = Smem<P, kWide, kLo>;
-  constexpr int WORDS = P / 8;
-  const int hh = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (hh >= S::H) return;
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
+template <typename T>
+__device__ __forceinline__ void load_q(const PagedAttendArgs& a, const T* q, bool live, float* x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = 0.f;
   if (live && lane * 4 < a.dim) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = Elem<T>::to_f32(q[lane * 4 + e]);
   }
+}
+template <int P, bool kWide, bool kLo>
+__device__ __forceinline__ void stage_q(const PagedAttendArgs& a, const float* x, int hh,
+                                        uint32_t* qw, float* fac) {
+  constexpr int WORDS = P / 8;
+  const int lane = threadIdx.x & 31;
   float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -422,11 +442,15 @@ __device__ __forceinline__ void stage_q(const PagedAttendArgs& a, const T* q, bo
     fac[hh] = a.scale * kToLog2 * pow2((9 - ex) / 2) * pow2((9 - ex) - (9 - ex) / 2);
 }
 
-__device__ __forceinline__ void finish(const PagedAttendArgs& a, int64_t row, int d, float m,
-                                       float l, float o) {
-  if (d < a.dim) a.out[row * a.dim + d] = l == 0.f ? 0.f : o / l;
-  if (d == 0 && a.lse != nullptr) a.lse[row] = l == 0.f ? -INFINITY : kToLn * (m + log2f(l));
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : kToLn * (m + log2f(l));
 }
+
+// Where the line of pairs is at: unit u = (kv head, chunk) of request r, pairs [u0, u0 + n).
+struct At {
+  int r, h, h0, nh;
+  uint32_t u, u0, n;
+};
 
 template <int P, bool kWide, typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(PagedAttendArgs a) {
@@ -435,16 +459,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   constexpr int G = P / 32, H = S::H, SB = strip_bytes(P), HL = kWide ? 2 : 1;
   extern __shared__ __align__(128) char sm[];
   float* slots = reinterpret_cast<float*>(sm + S::kSlots);
-  uint32_t* qw = reinterpret_cast<uint32_t*>(sm + S::kQ);
-  float* s_fac = reinterpret_cast<float*>(sm + S::kFac);
   int32_t* pre = reinterpret_cast<int32_t*>(sm + S::kPre);
+  uint16_t* cnt = reinterpret_cast<uint16_t*>(pre + a.R + 1);
   __shared__ int64_t s_w[kWarps];
   __shared__ int s_long;
-  __shared__ uint32_t s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int units = a.heads * a.chunks;  // per request
+  const uint32_t units = a.heads * a.chunks;  // per request
   char* ring = sm + warp * kStages * 2 * SB;
-  uint16_t* info = reinterpret_cast<uint16_t*>(sm + S::kInfo) + warp * 64;
+  uint64_t* where = reinterpret_cast<uint64_t*>(sm + S::kWhere) + warp * 64;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBars) + warp * kStages;
   if (lane < kStages) mbar_init(bars + lane, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -452,19 +474,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   if (tid == 0) s_long = 0;
   wait_for_stream();
 
-  // pairs of strips before each request (of one unit), and the longest unit
+  // pairs of strips (of one unit) and requests with any before each request; the longest unit
   int64_t run = 0;
   for (int base = 0; base < a.R; base += kThreads) {
     const int r = base + tid;
     int n = 0;
     if (r < a.R) n = (unit_map(a, paged_len(a.lens, r, a.bs, a.max_pages, a.status)).total() + 1) / 2;
     int64_t tot;
-    const int64_t ex = block_scan64(n, s_w, &tot);  // (two barriers: s_long is set by now)
-    if (r < a.R) pre[r] = static_cast<int32_t>(run + ex);
+    const int64_t ex =  // (two barriers: s_long is set by now)
+        run + block_scan64(int64_t(n) << 16 | int64_t(n > 0), s_w, &tot);
+    if (r < a.R) {
+      pre[r] = static_cast<int32_t>(ex >> 16);
+      cnt[r] = static_cast<uint16_t>(ex & 0xffff);
+    }
     if (n > 0) atomicMax(&s_long, n);
     run += tot;
   }
-  if (tid == 0) pre[a.R] = static_cast<int32_t>(run);
+  const uint32_t pairs = static_cast<uint32_t>(run >> 16), some = static_cast<uint32_t>(run & 0xffff);
+  if (tid == 0) {
+    pre[a.R] = static_cast<int32_t>(pairs);
+    cnt[a.R] = static_cast<uint16_t>(some);
+  }
   __syncthreads();
   // requests that attend to nothing
   for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
@@ -473,76 +503,138 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     for (int i = tid; i < hq * a.dim; i += kThreads) a.out[int64_t(r) * hq * a.dim + i] = 0.f;
     if (a.lse != nullptr)
       for (int i = tid; i < hq; i += kThreads) a.lse[int64_t(r) * hq + i] = -INFINITY;
+    for (int i = tid; i < static_cast<int>(units); i += kThreads)
+      a.units[int64_t(r) * units + i] = make_int2(0, 1);
   }
-  const uint32_t all = static_cast<uint32_t>(run) * units;
-  const uint32_t chunk = max((all + gridDim.x - 1) / gridDim.x,
-                             static_cast<uint32_t>(min(s_long, kLeast)));
-  const uint64_t first = uint64_t(chunk) * blockIdx.x;
-  if (first >= all) return;
-  const uint32_t begin = static_cast<uint32_t>(first), end = min(all, begin + chunk);
+  if (pairs == 0) return;
 
-  // the warp's pairs: begin + warp, + 8, ..
-  const int mine = static_cast<int>(end - begin) > warp
-                       ? static_cast<int>(end - begin - warp + kWarps - 1) / kWarps : 0;
-  const uint8_t* src = a.pool;  // of the lane's strip in the current round of 16 pairs
-  int valid = 0;
-  unsigned some = 0;            // lanes whose strip has rows to attend to
-  int dead_at = -1;             // the pair whose wait ran out: nothing is issued or awaited after
-  auto find = [&](int j0) {     // lane i finds strip i % 2 of pair j0 + i / 2
-    valid = 0;
-    const int j = j0 + lane / 2;
-    if (j < mine) {
-      const uint32_t at = begin + warp + uint32_t(j) * kWarps;
-      const int r = last_at_most(pre, a.R, static_cast<int32_t>(at / units));
-      const uint32_t n = pre[r + 1] - pre[r], in = at - uint32_t(pre[r]) * units, u = in / n;
-      const int v = 2 * static_cast<int>(in - u * n) + (lane & 1);
-      const UnitMap map = unit_map(a, a.lens[r]);
-      if (v < map.total())
-        src = locate(a, map, r, static_cast<int>(u) / a.chunks, v, SB, &valid);
-    }
-    some = __ballot_sync(0xffffffffu, valid != 0);
-    info[(2 * j0 + lane) & 63] = static_cast<uint16_t>(valid);
-    __syncwarp();
+  // (the same in every CTA)
+  const uint32_t longest = s_long, all = pairs * units;
+  const uint32_t share = (all + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
+  const bool alone = a.whole || longest <= kAloneParts * share || longest <= kAloneLeast;
+  const uint32_t extra = alone ? kAloneCost : kTeamCost;
+  const uint32_t cost = (pairs + extra * some) * units;
+  const uint32_t workers = alone ? gridDim.x * kWarps : gridDim.x;
+  const uint32_t worker = alone ? blockIdx.x * kWarps + warp : blockIdx.x;
+  const uint32_t chunk =
+      max((cost + workers - 1) / workers,
+          min(longest, static_cast<uint32_t>(alone ? kAloneLeast : kTeamLeast)) + extra);
+  if (!a.whole && uint64_t(chunk) * worker >= cost) return;
+
+  const auto place = [&](uint32_t at) {  // of a pair
+    At p;
+    p.r = last_at_most(pre, a.R, div(static_cast<int>(at), a.by_units));
+    p.n = pre[p.r + 1] - pre[p.r];
+    const uint32_t base = uint32_t(pre[p.r]) * units;
+    p.u = (at - base) / p.n;
+    p.u0 = base + p.u * p.n;
+    p.h = div(static_cast<int>(p.u), a.by_chunks);
+    p.h0 = (static_cast<int>(p.u) - p.h * a.chunks) * H;
+    p.nh = min(H, a.group - p.h0);
+    return p;
   };
-  auto issue = [&](int j) {  // pair j into its stage (which is free), by the lanes that found it
-    if (j >= mine) return;
-    if ((j & 15) == 0) find(j);
-    if (lane / 2 == (j & 15)) {
-      uint64_t* bar = bars + j % kStages;
-      if ((lane & 1) == 0) mbar_arrive_tx(bar, SB * __popc((some >> lane) & 3u));
-      if (valid != 0)
-        bulk_g2s(ring + ((j % kStages) * 2 + (lane & 1)) * SB, src, SB, bar);
+  const auto cost_at = [&](const At& p) {  // of a unit's first pair
+    return (uint32_t(pre[p.r]) + extra * cnt[p.r]) * units + p.u * (p.n + extra);
+  };
+  const auto pair_at = [&](uint32_t x) {  // the first pair whose cost is not below x
+    if (x >= cost) return all;
+    const uint32_t y = div(static_cast<int>(x), a.by_units);
+    int lo = 0, hi = a.R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (uint32_t(pre[mid]) + extra * cnt[mid] <= y) lo = mid;
+      else hi = mid;
+    }
+    const uint32_t n = pre[lo + 1] - pre[lo];
+    const uint32_t in = x - (uint32_t(pre[lo]) + extra * cnt[lo]) * units;
+    const uint32_t u = in / (n + extra);
+    return uint32_t(pre[lo]) * units + u * n + min(in - u * (n + extra), n);
+  };
+  const auto unit_at = [&](uint32_t i) {  // the first pair of the line's i-th unit
+    if (i >= some * units) return all;
+    const uint32_t k = div(static_cast<int>(i), a.by_units);
+    int lo = 0, hi = a.R;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cnt[mid] <= k) lo = mid;
+      else hi = mid;
+    }
+    return uint32_t(pre[lo]) * units + (i - k * units) * uint32_t(pre[lo + 1] - pre[lo]);
+  };
+  uint32_t begin, end;
+  if (a.whole) {
+    begin = unit_at(static_cast<uint32_t>(uint64_t(some) * units * worker / workers));
+    end = unit_at(static_cast<uint32_t>(uint64_t(some) * units * (worker + 1) / workers));
+  } else {
+    begin = pair_at(chunk * worker);
+    end = uint64_t(chunk) * (worker + 1) >= cost ? all : pair_at(chunk * (worker + 1));
+  }
+  if (begin >= end) return;  // (no pair among what it was dealt)
+
+  // the warp's pairs: begin + warp, + 8, .. of the CTA's, or all of its own
+  const uint32_t turn = alone ? begin : begin + warp, stride = alone ? 1 : kWarps;
+  const int mine = turn < end ? static_cast<int>((end - turn + stride - 1) / stride) : 0;
+  bool dead = false;  // a wait ran out: nothing is issued or awaited after
+  const auto issue = [&](int n) {  // the warp's n-th pair into stage n % 2, which is free
+    if (n >= mine) return;
+    if ((n & 15) == 0) {  // lane i finds strip i % 2 of pair n + i / 2
+      const int i = n + lane / 2;
+      uint64_t e = 0;
+      if (i < mine) {
+        const uint32_t at = turn + uint32_t(i) * stride;
+        const At p = place(at);
+        const int v = 2 * static_cast<int>(at - p.u0) + (lane & 1);
+        const UnitMap map = unit_map(a, a.lens[p.r]);
+        if (v < map.total()) e = locate(a, map, p.r, p.h, v, SB);
+      }
+      where[(2 * n + lane) & 63] = e;
+      __syncwarp();
+    }
+    if (lane < 2) {
+      const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(where + ((2 * n) & 63));
+      uint64_t* bar = bars + n % kStages;
+      if (lane == 0) mbar_arrive_tx(bar, SB * ((e.x != 0) + (e.y != 0)));
+      const uint64_t x = lane == 0 ? e.x : e.y;
+      if (x != 0)
+        bulk_g2s(ring + ((n % kStages) * 2 + lane) * SB, a.pool + (x & 0xffffffffffffull), SB, bar);
     }
   };
+  uint32_t* qw = reinterpret_cast<uint32_t*>(
+      alone ? sm + S::kSlots + warp * S::kSlot * 4 : sm + S::kQ);
+  float* s_fac = reinterpret_cast<float*>(sm + S::kFac) + (alone ? warp * 8 : 0);
+  const auto fetch = [&](const At& p, int hh, float* x) {
+    load_q(a, static_cast<const T*>(a.q) + p.r * a.q_req +
+                  (int64_t(p.h) * a.group + p.h0 + hh) * a.q_head, hh < p.nh, x);
+  };
+  const auto stage = [&](const At& p, int hh) {
+    float x[4];
+    fetch(p, hh, x);
+    stage_q<P, kWide, kLo>(a, x, hh, qw, s_fac);
+  };
+
 #pragma unroll 1
-  for (int j = 0; j < kStages; ++j) issue(j);
+  for (int n = 0; n < kStages; ++n) issue(n);
+  if (!alone) {
+    if (warp < H) stage(place(begin), warp);
+    __syncthreads();
+  }
 
   int j = 0;  // the warp's next pair
   for (uint32_t at = begin; at < end;) {
-    const int r = last_at_most(pre, a.R, static_cast<int32_t>(at / units));
-    const uint32_t n = pre[r + 1] - pre[r], base = uint32_t(pre[r]) * units;
-    const uint32_t u = (at - base) / n;
-    const int h = static_cast<int>(u) / a.chunks, h0 = (static_cast<int>(u) - h * a.chunks) * H;
-    const uint32_t u0 = base + u * n;             // the unit's first pair
-    const uint32_t stop = min(end, u0 + n);
-    const int nh = min(H, a.group - h0);
+    uint32_t stop;
     {
-      const int hh = warp;
-      stage_q<P, kWide, kLo>(a,
-                             static_cast<const T*>(a.q) + r * a.q_req +
-                                 (int64_t(h) * a.group + h0 + hh) * a.q_head,
-                             hh < nh, qw, s_fac);
-    }
-    __syncthreads();
-    QFrag<P, kWide, kLo> qf;
+      const At p = place(at);
+      stop = min(end, p.u0 + p.n);
+      if (alone) {
+        float x[H][4];
 #pragma unroll
-    for (int p = 0; p < QFrag<P, kWide, kLo>::kParts; ++p)
+        for (int hh = 0; hh < H; ++hh) fetch(p, hh, x[hh]);
+        __syncwarp();
 #pragma unroll
-      for (int w = 0; w < P / 32; ++w) {
-        const uint4 x = *reinterpret_cast<const uint4*>(qw + ((p * (P / 32) + w) * 32 + lane) * 4);
-        qf.w[p][4 * w] = x.x; qf.w[p][4 * w + 1] = x.y;
-        qf.w[p][4 * w + 2] = x.z; qf.w[p][4 * w + 3] = x.w;
+        for (int hh = 0; hh < H; ++hh) stage_q<P, kWide, kLo>(a, x[hh], hh, qw, s_fac);
+        __syncwarp();
       }
+    }
     float fac[HL];
     State<P, kWide> st;
     st.e = kMostE;
@@ -559,175 +651,205 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       for (int i = 0; i < 4; ++i) st.acc[b][i] = 0.f;
 
 #pragma unroll 1
-    for (; j < mine && begin + warp + uint32_t(j) * kWarps < stop; ++j) {
-      const int stage = j % kStages;
-      if (dead_at >= 0) continue;
+    for (; j < mine && turn + uint32_t(j) * stride < stop; ++j) {
+      if (dead) continue;
       const uint32_t parity = (j / kStages) & 1;
-      bool ok = mbar_try(bars + stage, parity);
+      uint64_t* bar = bars + j % kStages;
+      bool ok = mbar_try(bar, parity);
       if (!__all_sync(0xffffffffu, ok)) {
         const unsigned long long t0 = now_ns();
         do {
-          if (!ok) ok = mbar_try(bars + stage, parity);
+          if (!ok) ok = mbar_try(bar, parity);
         } while (!__all_sync(0xffffffffu, ok) &&
                  !__shfl_sync(0xffffffffu, now_ns() - t0 > kTimeoutNs, 0));
         if (!__all_sync(0xffffffffu, ok)) {
           if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, j);
-          dead_at = j;
+          // copies in flight land before the warp goes on without its pairs
+          mbar_drain(bar, parity);
+          if (j + 1 < mine) mbar_drain(bars + (j + 1) % kStages, ((j + 1) / kStages) & 1);
+          dead = true;
           continue;
         }
       }
-      const int v0 = info[(2 * j) & 63], v1 = info[(2 * j + 1) & 63];
+      const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(where + ((2 * j) & 63));
+      const int v0 = static_cast<int>(e.x >> 48), v1 = static_cast<int>(e.y >> 48);
       if (v0 | v1)
-        pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + stage * 2 * SB), v0, v1,
-                                 qf, fac, st);
+        pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + (j % kStages) * 2 * SB), v0,
+                                 v1, qw, fac, st);
       __syncwarp();
       issue(j + kStages);
     }
 
-    // warp states to shared memory
+    // the warp's state, in its lanes: dims 32 g + 4 t + {0..3} of heads HL c ..
+    const int t = lane >> 2, c = lane & 3;
+    float4 o[HL][G];
     {
-      const int t = lane >> 2, c = lane & 3;
       const float down = pow2(-st.e);
 #pragma unroll
       for (int i = 0; i < HL; ++i) {
-        float l = st.l[i];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float* s = slots + warp * S::kSlot + (HL * c + i) * S::kRow;
+        for (int x = 4; x < 32; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const float* d0 = st.acc[2 * g];
-          const float* d1 = st.acc[2 * g + 1];
-          float4 o;
-          if constexpr (kWide) {
-            o = make_float4(d0[i], d0[2 + i], d1[i], d1[2 + i]);
-          } else {
-            o = make_float4(d0[0] + d0[1], d0[2] + d0[3], d1[0] + d1[1], d1[2] + d1[3]);
+          float y[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float* d = st.acc[2 * g + x / 2];
+            y[x] = (kWide ? d[2 * (x % 2) + i] : d[2 * (x % 2)] + d[2 * (x % 2) + 1]) * 0x1p9f * down;
           }
-          *reinterpret_cast<float4*>(s + 32 * g + 4 * t) =
-              make_float4(o.x * 0x1p9f * down, o.y * 0x1p9f * down, o.z * 0x1p9f * down,
-                          o.w * 0x1p9f * down);
+          o[i][g] = make_float4(y[0], y[1], y[2], y[3]);
         }
+      }
+    }
+    const bool more = stop < end;
+    const At p = place(at);  // (again: nothing of it is kept over the loop)
+    const bool whole = at == p.u0 && stop == p.u0 + p.n;
+    const int64_t row0 = (int64_t(p.r) * a.heads + p.h) * a.group + p.h0;
+    float* part = a.parts + (int64_t(worker) * 2 + (at == begin ? 0 : 1)) * S::kSlot;
+    float* to = alone ? part : slots + warp * S::kSlot;
+    if (at == p.u0 && lane == 0 && (alone || warp == 0)) {
+      // this worker holds the unit's first pair; the last one's holds its last
+      const uint32_t x0 = cost_at(p);
+      a.units[int64_t(p.r) * units + p.u] =
+          whole ? make_int2(0, 1)
+                : make_int2(static_cast<int>(worker) * 2 + (at == begin ? 0 : 1),
+                            static_cast<int>((x0 + p.n - 1) / chunk - x0 / chunk) + 1);
+    }
+    if (!(alone && whole)) {
+#pragma unroll
+      for (int i = 0; i < HL; ++i) {
+        if (alone && HL * c + i >= p.nh) continue;
+        float* s = to + (HL * c + i) * S::kRow;
+#pragma unroll
+        for (int g = 0; g < G; ++g) *reinterpret_cast<float4*>(s + 32 * g + 4 * t) = o[i][g];
         if (t == 0) {
           s[P] = st.m[i];
-          s[P + 1] = l;
+          s[P + 1] = st.l[i];
         }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < HL; ++i) {
+        const int hh = HL * c + i;
+        if (hh >= p.nh) continue;
+        const float l = st.l[i], r = l == 0.f ? 0.f : 1.f / l;
+        float* out = a.out + (row0 + hh) * a.dim;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int d = 32 * g + 4 * t;
+          if (d >= a.dim) continue;
+          out[d] = o[i][g].x * r;
+          out[d + 1] = o[i][g].y * r;
+          out[d + 2] = o[i][g].z * r;
+          out[d + 3] = o[i][g].w * r;
+        }
+        if (t == 0 && a.lse != nullptr) a.lse[row0 + hh] = lse_of(st.m[i], l);
       }
     }
-    __syncthreads();
-
-    const bool whole = at == u0 && stop == u0 + n;
-    const int64_t row0 = (int64_t(r) * a.heads + h) * a.group + h0;
-    float* part = a.parts + (int64_t(blockIdx.x) * 2 + (at == begin ? 0 : 1)) * S::kSlot;
-    for (int i = tid; i < nh * P; i += kThreads) {
-      const int hh = i / P, d = i % P;
-      const float* s = slots + hh * S::kRow;
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s[w * S::kSlot + P]);
-      float l = 0.f, o = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float pm = s[w * S::kSlot + P];
-        const float f = pm == m ? 1.f : ex2(pm - m);
-        l += f * s[w * S::kSlot + P + 1];
-        o += f * s[w * S::kSlot + d];
-      }
-      if (whole) {
-        finish(a, row0 + hh, d, m, l, o);
-      } else {
-        float* to = part + hh * S::kRow;
-        to[d] = o;
-        if (d == 0) {
-          to[P] = m;
-          to[P + 1] = l;
-        }
-      }
-    }
-    if (!whole) {
-      // the unit's CTAs: i0 holds its first pair, i1 its last
-      const int i0 = u0 / chunk, i1 = (u0 + n - 1) / chunk;
-      __threadfence();
+    if (!alone) {
       __syncthreads();
-      if (tid == 0) {
-        uint32_t* ticket = a.tickets + int64_t(r) * units + u;
-        s_last = atom_add_acq_rel(ticket, 1) == static_cast<uint32_t>(i1 - i0);
-        if (s_last) *ticket = 0;
-      }
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        // Warps take rows and shares of the parts, eight parts' loads in flight; the shares meet
-        // in shared memory.  (i0's part is its second one unless its range starts the unit.)
-        const float* p0 = a.parts + (int64_t(i0) * 2 + (uint64_t(chunk) * i0 >= u0 ? 0 : 1)) * S::kSlot;
-        const float* p1 = a.parts + int64_t(i0) * 2 * S::kSlot;
-        constexpr int kShares = kWarps / H;
-        const int hh = warp % H, share = warp / H, np = i1 - i0 + 1;
-        if (hh < nh) {
-          float m = -INFINITY, l = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int kU = 8;
-          for (int c0 = share; c0 < np; c0 += kU * kShares) {
-            float pm[kU], pl[kU];
-            float4 po[kU];
+      if (more && warp < H) stage(place(stop), warp);  // (every warp is done with this unit's)
+      for (int i = tid; i < p.nh * P; i += kThreads) {
+        const int hh = i / P, d = i % P;
+        const float* s = slots + hh * S::kRow;
+        float m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kU; ++i) {
-              const int c = c0 + i * kShares;
-              pm[i] = -INFINITY;
-              pl[i] = 0.f;
-              po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (c < np) {
-                const float* s = (c == 0 ? p0 : p1 + int64_t(c) * 2 * S::kSlot) + hh * S::kRow;
-                pm[i] = __ldcg(s + P);
-                pl[i] = __ldcg(s + P + 1);
-                if (lane * 4 < P) po[i] = __ldcg(reinterpret_cast<const float4*>(s) + lane);
-              }
-            }
-            float top = m;
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s[w * S::kSlot + P]);
+        float l = 0.f, x = 0.f;
 #pragma unroll
-            for (int i = 0; i < kU; ++i) top = fmaxf(top, pm[i]);
-            const float f0 = m == top ? 1.f : ex2(m - top);
-            l *= f0;
-            o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
-            m = top;
-#pragma unroll
-            for (int i = 0; i < kU; ++i) {
-              const float f = pm[i] == top ? 1.f : ex2(pm[i] - top);
-              l += f * pl[i];
-              o.x += f * po[i].x; o.y += f * po[i].y; o.z += f * po[i].z; o.w += f * po[i].w;
-            }
-          }
-          float* s = slots + (share * H + hh) * S::kRow;
-          if (lane * 4 < P) *reinterpret_cast<float4*>(s + lane * 4) = o;
-          if (lane == 0) {
-            s[P] = m;
-            s[P + 1] = l;
-          }
+        for (int w = 0; w < kWarps; ++w) {
+          const float pm = s[w * S::kSlot + P];
+          const float f = pm == m ? 1.f : ex2(pm - m);
+          l += f * s[w * S::kSlot + P + 1];
+          x += f * s[w * S::kSlot + d];
         }
-        __syncthreads();
-        for (int i = tid; i < nh * P; i += kThreads) {
-          const int row = i / P, d = i % P;
-          const float* s = slots + row * S::kRow;
-          float m = -INFINITY, l = 0.f, o = 0.f;
-#pragma unroll
-          for (int w = 0; w < kShares; ++w) m = fmaxf(m, s[w * S::kSlot + P]);
-#pragma unroll
-          for (int w = 0; w < kShares; ++w) {
-            const float f = s[w * S::kSlot + P] == m ? 1.f : ex2(s[w * S::kSlot + P] - m);
-            l += f * s[w * S::kSlot + P + 1];
-            o += f * s[w * S::kSlot + d];
+        if (whole) {
+          if (d < a.dim) a.out[(row0 + hh) * a.dim + d] = l == 0.f ? 0.f : x / l;
+          if (d == 0 && a.lse != nullptr) a.lse[row0 + hh] = lse_of(m, l);
+        } else {
+          float* y = part + hh * S::kRow;
+          y[d] = x;
+          if (d == 0) {
+            y[P] = m;
+            y[P + 1] = l;
           }
-          finish(a, row0 + row, d, m, l, o);
         }
       }
     }
     at = stop;
+    if (!alone && more) __syncthreads();  // the slots are read, q of the next unit is there
   }
-  if (dead_at >= 0) {  // copies in flight land before the CTA leaves
-    const int last = min(mine, dead_at + kStages) - 1;
-    for (int s = 0; s < kStages && s <= last; ++s)
-      mbar_drain(bars + s, ((last - (last - s) % kStages) / kStages) & 1);
+}
+
+// Merges the parts of one (request, q head): four warps take every fourth part, eight parts' loads
+// in flight, and meet in shared memory.  The first part of a unit may be its worker's second; the
+// others are the following workers' first.
+constexpr int kMergeWarps = 4;
+template <int P>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(PagedAttendArgs a, int H) {
+  constexpr int kRow = P + 4, kU = 8;
+  __shared__ __align__(16) float s_part[kMergeWarps][kRow];
+  wait_for_stream();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int hq = a.heads * a.group, r = blockIdx.x / hq, head = blockIdx.x - r * hq;
+  const int h = head / a.group, in = head - h * a.group, chunk = in / H, hh = in - chunk * H;
+  const int2 u = a.units[int64_t(r) * a.heads * a.chunks + h * a.chunks + chunk];
+  if (u.y <= 1) return;
+  const float* p0 = a.parts + (int64_t(u.x) * H + hh) * kRow;
+  const float* p1 = a.parts + (int64_t(u.x / 2) * 2 * H + hh) * kRow;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = warp; c0 < u.y; c0 += kU * kMergeWarps) {
+    float pm[kU], pl[kU];
+    float4 po[kU];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const int c = c0 + i * kMergeWarps;
+      pm[i] = -INFINITY;
+      pl[i] = 0.f;
+      po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < u.y) {
+        const float* s = c == 0 ? p0 : p1 + int64_t(c) * 2 * H * kRow;
+        pm[i] = s[P];
+        pl[i] = s[P + 1];
+        if (lane * 4 < P) po[i] = reinterpret_cast<const float4*>(s)[lane];
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kU; ++i) top = fmaxf(top, pm[i]);
+    const float f0 = m == top ? 1.f : ex2(m - top);
+    l *= f0;
+    o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+    m = top;
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const float f = pm[i] == top ? 1.f : ex2(pm[i] - top);
+      l += f * pl[i];
+      o.x += f * po[i].x; o.y += f * po[i].y; o.z += f * po[i].z; o.w += f * po[i].w;
+    }
   }
+  if (lane * 4 < P) *reinterpret_cast<float4*>(&s_part[warp][lane * 4]) = o;
+  if (lane == 0) {
+    s_part[warp][P] = m;
+    s_part[warp][P + 1] = l;
+  }
+  __syncthreads();
+  const int d = threadIdx.x;
+  m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) m = fmaxf(m, s_part[w][P]);
+  float x = 0.f;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = s_part[w][P] == m ? 1.f : ex2(s_part[w][P] - m);
+    l += f * s_part[w][P + 1];
+    x += f * (d < P ? s_part[w][d] : 0.f);
+  }
+  const int64_t row = int64_t(r) * hq + head;
+  if (d < a.dim) a.out[row * a.dim + d] = l == 0.f ? 0.f : x / l;
+  if (d == 0 && a.lse != nullptr) a.lse[row] = lse_of(m, l);
 }
 
 // Groups of up to four q heads to a kv head take the packed form, larger ones the wide one.
@@ -736,8 +858,8 @@ int chunks_of(const rba_paged* s) {
   const int group = s->d.n_q_heads / s->d.n_kv_heads;
   return group <= 4 ? 1 : (group + 7) / 8;
 }
-size_t ticket_bytes(const rba_paged* s) {
-  return align_up(size_t(s->d.max_requests) * s->d.n_kv_heads * chunks_of(s) * 4, 256);
+size_t unit_bytes(const rba_paged* s) {
+  return align_up(size_t(s->d.max_requests) * s->d.n_kv_heads * chunks_of(s) * sizeof(int2), 256);
 }
 
 template <int P, bool kWide, typename T>
@@ -747,6 +869,10 @@ rba_status launch(const PagedAttendArgs& a, cudaStream_t stream) {
   RBA_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kernel), smem));
   RBA_CUDA_TRY(launch_dependent(kernel, static_cast<unsigned>(num_sms() * kCtasPerSm), kThreads,
                                 smem, stream, a));
+  if (!a.whole)
+    RBA_CUDA_TRY(launch_dependent(paged_merge_kernel<P>,
+                                  static_cast<unsigned>(a.R * a.heads * a.group), kMergeWarps * 32,
+                                  0, stream, a, kWide ? 8 : 4));
   return RBA_OK;
 }
 
@@ -756,8 +882,8 @@ rba_status launch(const PagedAttendArgs& a, cudaStream_t stream) {
 extern "C" size_t rba_paged_attend_workspace_size(const rba_paged* s) {
   using namespace rba;
   if (s == nullptr) return 0;
-  return ticket_bytes(s) + size_t(num_sms()) * kCtasPerSm * 2 * (wide_of(s) ? 8 : 4) *
-                               (s->pitch + 4) * sizeof(float);
+  return unit_bytes(s) + size_t(num_sms()) * kCtasPerSm * kWarps * 2 *
+                               (wide_of(s) ? 8 : 4) * (s->pitch + 4) * sizeof(float);
 }
 
 extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
@@ -773,10 +899,11 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
     return RBA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return RBA_ERR_INVALID_ARG;
   if (ws_bytes < rba_paged_attend_workspace_size(s)) return RBA_ERR_WORKSPACE;
-  // the line of strips is counted in 32 bits (sink, selection and window can share two pages)
-  const int64_t line = int64_t(n_requests) * (int64_t(s->d.max_pages) + 2) * s->strips;
-  if (line > INT32_MAX || line * s->d.n_kv_heads * chunks_of(s) > INT32_MAX)
-    return RBA_ERR_UNSUPPORTED;
+  // the line of pairs, with what units cost, is counted in 31 bits (sink, selection and window can
+  // share two pages)
+  const int64_t unit = ((int64_t(s->d.max_pages) + 2) * s->strips + 1) / 2 + kTeamCost;
+  const int64_t units = int64_t(n_requests) * s->d.n_kv_heads * chunks_of(s);
+  if (unit > INT32_MAX || unit * units > INT32_MAX) return RBA_ERR_UNSUPPORTED;
   PagedAttendArgs a = {};
   a.q = q;
   a.q_req = q_request_stride;
@@ -788,8 +915,8 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
   a.status = s->b.status;
   a.out = out;
   a.lse = lse;
-  a.tickets = static_cast<uint32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + ticket_bytes(s));
+  a.units = static_cast<int2*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + unit_bytes(s));
   a.scale = scale;
   a.R = n_requests;
   a.heads = s->d.n_kv_heads;
@@ -803,6 +930,16 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
   a.sink = sink;
   a.window = window;
   a.chunks = chunks_of(s);
+  a.first = sink / a.bs;
+  // the longest unit there can be: what sink, selection and window ask for, or the whole table
+  const int64_t strips = std::min<int64_t>(
+      int64_t(sink) / kStrip + int64_t(k) * s->strips + int64_t(window) / kStrip + 4 * s->strips,
+      int64_t(s->d.max_pages) * s->strips);
+  a.whole = (strips + 1) / 2 <= kWholePairs;
+  a.by_bs = fast_div(a.bs);
+  a.by_strips = fast_div(a.strips);
+  a.by_units = fast_div(a.heads * a.chunks);
+  a.by_chunks = fast_div(a.chunks);
   const bool bf = s->d.dtype == RBA_BF16;
   if (s->pitch == 128) {
     if (wide_of(s))

@@ -667,10 +667,10 @@ class PagedStore:
         return idx
 
     def attend_workspace(self):
-        """Zeroed workspace of attend; one serves every call, one call at a time."""
+        """Workspace of attend; one serves every call, one call at a time."""
         with torch.cuda.device(self.device):
             n = lib().rba_paged_attend_workspace_size(self.handle)
-        return torch.zeros(max(n, 16), dtype=torch.uint8, device=self.device)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
 
     def attend(self, q, idx, sink, window, *, scale=None, out=None, lse=None, workspace=None):
         """Attention of one token of each request, q [R][Hq][D], over its sink tokens, the
