@@ -32,7 +32,7 @@
 // would change from run to run.)  A worker's part of a unit that it does not hold whole goes to
 // the workspace, and a second kernel merges each unit's parts in order: cheaper than a ticket, a
 // fence and a merge by the last worker to arrive, which few warps would then wait for.  Where no
-// unit can be longer than kWholePairs, warps take whole units and there is no second kernel.
+// unit can be longer than kWholePairs, workers take whole units and there is no second kernel.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -53,6 +53,8 @@ constexpr int kTeamCost = 8, kAloneCost = 2;
 constexpr int kTeamLeast = kWarps, kAloneLeast = 2;
 // Warps work alone where the longest unit is then cut into at most this many parts.
 constexpr int kAloneParts = 24;
+// Units are taken whole where none can be longer than this: by single warps, or by CTAs where those
+// suffice for one unit each.
 constexpr int kWholePairs = 8;
 constexpr float kToLog2 = 1.4426950408889634f;
 constexpr float kToLn = 0.6931471805599453f;
@@ -76,7 +78,7 @@ struct PagedAttendArgs {
   int R, heads, group, dim, bs, strips, max_pages, n_pages, k, sink, window;
   int chunks;         // head chunks of a kv head
   int first;          // sink / bs
-  int whole;          // warps take whole units
+  int whole;          // workers take whole units
   FastDiv by_bs, by_strips, by_units, by_chunks;
 };
 
@@ -186,6 +188,20 @@ __device__ __forceinline__ uint64_t locate(const PagedAttendArgs& a, const UnitM
          uint64_t(ra + 32 * rb) << 48;
 }
 
+// The same for one byte of each half word (0: the low ones): the codes of its low nibbles, and
+// low + 16 high in one number.  For a product's rows this saves the shift: the second row of a pair
+// gathers the sum for low + 16 high, and the difference is taken once, at the end.
+template <int kByte>
+__device__ __forceinline__ void codes_of_bytes(uint32_t w, uint32_t* low, uint32_t* both) {
+  const uint32_t b = __byte_perm(w, 0, kByte ? 0x4341 : 0x4240);
+  const uint32_t up = 0x78007800u, off = 0xb440b440u;  // 2^15, -136 2^-9, twice
+  const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&up),
+                            *reinterpret_cast<const __half2*>(&off));
+  *low = codes2<0>(b);
+  *both = *reinterpret_cast<const uint32_t*>(&y);
+}
+
 // The G words of a lane at p.
 template <int G> __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   if constexpr (G == 4) {
@@ -209,7 +225,7 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // (a 
 // Parts of the q operand (in shared memory, read group by group): hi, and for wide 32-bit q lo.
 template <bool kWide, bool kLo> constexpr int q_parts() { return kWide && kLo ? 2 : 1; }
 
-// A warp's running state for the unit's heads; lane (t, c) = (lane / 4, lane % 4) holds head c
+// A warp's running state for the unit's heads (y: logits over fac >= 0, in log2 units); lane (t, c) = (lane / 4, lane % 4) holds head c
 // (packed) or heads 2 c and 2 c + 1 (wide).  A weight is 2^(y - m), y the logit in log2 units;
 // the values' scales are taken times 2^e, which keeps weight x scale within a half's range.
 template <int P, bool kWide> struct State {
@@ -217,7 +233,9 @@ template <int P, bool kWide> struct State {
   float m[HL], l[HL];    // reference; this lane's part of the weights' sum
   float top[HL];         // a logit above it moves the reference
   float most;            // a scale above it moves e
-  float acc[2 * G][4];   // dims 32 g + 4 t + {0..3}: packed hi and lo columns, wide two heads
+  // dims 32 g + 4 t + {0, 1 (plus 16 times it), 2, 3 (the same)}: packed hi and lo columns, wide
+  // two heads
+  float acc[2 * G][4];
   int e;
 };
 
@@ -263,14 +281,11 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
           y[0][n][half] = fmaf(s, d[2 * half], y[0][n][half]);
           y[HL - 1][n][half] = fmaf(s, d[2 * half + 1], y[HL - 1][n][half]);
         } else {
-          y[0][n][half] = fmaf(s, d[2 * half] + d[2 * half + 1], y[0][n][half]);
+          // (a bf16 q has no lo part)
+          y[0][n][half] = fmaf(s, kLo ? d[2 * half] + d[2 * half + 1] : d[2 * half], y[0][n][half]);
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < HL; ++i)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) y[i][n][half] *= fac[i];
   }
   if (!whole) {  // rows outside the attended set: no weight, and nothing of their scales
 #pragma unroll
@@ -295,7 +310,7 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
   float ymax[HL];
 #pragma unroll
   for (int i = 0; i < HL; ++i) {
-    ymax[i] = fmaxf(fmaxf(y[i][0][0], y[i][0][1]), fmaxf(y[i][1][0], y[i][1][1]));
+    ymax[i] = fmaxf(fmaxf(y[i][0][0], y[i][0][1]), fmaxf(y[i][1][0], y[i][1][1])) * fac[i];
     grow |= ymax[i] > st.top[i];
   }
   if (__any_sync(0xffffffffu, grow)) {
@@ -330,7 +345,7 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float p = ex2(y[i][n][half] - st.m[i]);
+        float p = ex2(fmaf(y[i][n][half], fac[i], -st.m[i]));
         // (a row without weight before any row with one: -infinity against -infinity)
         if (!whole) p = y[i][n][half] == -INFINITY ? 0.f : p;
         st.l[i] += p;
@@ -345,9 +360,12 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       // codes of the group's two 16-dim tiles
-      const uint32_t w0 = v[0][g], w1 = v[1][g], u0 = w0 >> 8, u1 = w1 >> 8;
-      const uint32_t a0[4] = {codes2<0>(w0), codes2<1>(w0), codes2<0>(w1), codes2<1>(w1)};
-      const uint32_t a1[4] = {codes2<0>(u0), codes2<1>(u0), codes2<0>(u1), codes2<1>(u1)};
+      uint32_t a0[4], a1[4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        codes_of_bytes<0>(v[half][g], a0 + 2 * half, a0 + 2 * half + 1);
+        codes_of_bytes<1>(v[half][g], a1 + 2 * half, a1 + 2 * half + 1);
+      }
       // weights with the group's scale, hi + lo halves (11 + 11 bits)
       float hi[HL][2], lo[HL][2];
 #pragma unroll
@@ -417,8 +435,8 @@ __device__ __forceinline__ void stage_q(const PagedAttendArgs& a, const float* x
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const int ex = top > 0.f ? 14 - exponent(top) : 0;
-  // (two factors: 2^ex alone can leave the range of a float)
-  const float up0 = pow2(ex / 2), up1 = pow2(ex - ex / 2);
+  // (two factors: 2^ex alone can leave the range of a float; the scale's sign goes with q)
+  const float up0 = copysignf(pow2(ex / 2), a.scale), up1 = pow2(ex - ex / 2);
   const int g = lane >> 3, c = (lane & 7) >> 1, odd = lane & 1;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -439,7 +457,18 @@ __device__ __forceinline__ void stage_q(const PagedAttendArgs& a, const float* x
     qw[((part * (WORDS / 4) + w / 4) * 32 + t * 4 + c) * 4 + w % 4] = word;
   }
   if (lane == 0)
-    fac[hh] = a.scale * kToLog2 * pow2((9 - ex) / 2) * pow2((9 - ex) - (9 - ex) / 2);
+    fac[hh] = fabsf(a.scale) * kToLog2 * pow2((9 - ex) / 2) * pow2((9 - ex) - (9 - ex) / 2);
+}
+
+// The operand's columns of a head that is not there.
+template <int P, bool kWide, bool kLo>
+__device__ __forceinline__ void zero_q(int hh, uint32_t* qw, float* fac) {
+  const int lane = threadIdx.x & 31, cols = kWide ? 1 : 2;
+  for (int i = lane; i < q_parts<kWide, kLo>() * (P / 32) * cols * 4; i += 32) {
+    const int c = i % 4, t = hh * cols + i / 4 % cols, w = i / 4 / cols;
+    *reinterpret_cast<uint4*>(qw + (w * 32 + t * 4 + c) * 4) = make_uint4(0, 0, 0, 0);
+  }
+  if (lane == 0) fac[hh] = 0.f;
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -511,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   // (the same in every CTA)
   const uint32_t longest = s_long, all = pairs * units;
   const uint32_t share = (all + gridDim.x * kWarps - 1) / (gridDim.x * kWarps);
-  const bool alone = a.whole || longest <= kAloneParts * share || longest <= kAloneLeast;
+  const bool alone = a.whole ? some * units > gridDim.x : longest <= kAloneParts * share;
   const uint32_t extra = alone ? kAloneCost : kTeamCost;
   const uint32_t cost = (pairs + extra * some) * units;
   const uint32_t workers = alone ? gridDim.x * kWarps : gridDim.x;
@@ -631,7 +660,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
         for (int hh = 0; hh < H; ++hh) fetch(p, hh, x[hh]);
         __syncwarp();
 #pragma unroll
-        for (int hh = 0; hh < H; ++hh) stage_q<P, kWide, kLo>(a, x[hh], hh, qw, s_fac);
+        for (int hh = 0; hh < H; ++hh) {
+          if (hh < p.nh) stage_q<P, kWide, kLo>(a, x[hh], hh, qw, s_fac);
+          else zero_q<P, kWide, kLo>(hh, qw, s_fac);
+        }
         __syncwarp();
       }
     }
@@ -697,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
             const float* d = st.acc[2 * g + x / 2];
             y[x] = (kWide ? d[2 * (x % 2) + i] : d[2 * (x % 2)] + d[2 * (x % 2) + 1]) * 0x1p9f * down;
           }
-          o[i][g] = make_float4(y[0], y[1], y[2], y[3]);
+          // (the odd rows hold the even dim plus 16 times theirs)
+          o[i][g] = make_float4(y[0], (y[1] - y[0]) * 0.0625f, y[2], (y[3] - y[2]) * 0.0625f);
         }
       }
     }
