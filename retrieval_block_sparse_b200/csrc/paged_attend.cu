@@ -49,7 +49,7 @@ constexpr int kCtasPerSm = 2;
 constexpr int kStages = 2;  // pairs of strips in a warp's ring
 // What a unit's start and end cost, in pairs of its worker, and the pairs that a worker takes at
 // least (or a whole unit): for CTAs and for single warps.
-constexpr int kTeamCost = 8, kAloneCost = 2;
+constexpr int kTeamCost = 10, kAloneCost = 3;
 constexpr int kTeamLeast = kWarps, kAloneLeast = 2;
 // Warps work alone where the longest unit is then cut into at most this many parts.
 constexpr int kAloneParts = 24;
@@ -396,7 +396,8 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
 }
 
 // Shared memory: rings | warp states (warps working alone: their q operands) | q operand |
-// factors | where strips lie | barriers | pairs and units before each request.
+// factors | barriers | pairs and units before each request.  (With up to 590 requests two CTAs fit an
+// SM in every form.)
 template <int P, bool kWide, bool kLo> struct Smem {
   static constexpr int H = kWide ? 8 : 4;
   static constexpr int kRow = P + 4;            // out, then m and l
@@ -406,8 +407,7 @@ template <int P, bool kWide, bool kLo> struct Smem {
   static constexpr int kSlots = kRing;
   static constexpr int kQ = kSlots + kWarps * kSlot * 4;
   static constexpr int kFac = kQ + kQBytes;
-  static constexpr int kWhere = kFac + kWarps * 32;
-  static constexpr int kBars = kWhere + kWarps * 64 * 8;
+  static constexpr int kBars = kFac + kWarps * 32;
   static constexpr int kPre = kBars + kWarps * kStages * 8;
   static_assert(kQBytes <= kSlot * 4, "a warp's q operand fits its state's place");
   static size_t bytes(int R) { return kPre + size_t(R + 1) * 6; }
@@ -492,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   uint16_t* cnt = reinterpret_cast<uint16_t*>(pre + a.R + 1);
   __shared__ int64_t s_w[kWarps];
   __shared__ int s_long;
+  __shared__ uint32_t s_chunk;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t units = a.heads * a.chunks;  // per request
   char* ring = sm + warp * kStages * 2 * SB;
-  uint64_t* where = reinterpret_cast<uint64_t*>(sm + S::kWhere) + warp * 64;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBars) + warp * kStages;
   if (lane < kStages) mbar_init(bars + lane, 1);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -548,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   const uint32_t chunk =
       max((cost + workers - 1) / workers,
           min(longest, static_cast<uint32_t>(alone ? kAloneLeast : kTeamLeast)) + extra);
+  if (lane == 0) s_chunk = chunk;  // (every warp the same value: its own lanes read it back)
   if (!a.whole && uint64_t(chunk) * worker >= cost) return;
 
   const auto place = [&](uint32_t at) {  // of a pair
@@ -604,28 +605,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   const uint32_t turn = alone ? begin : begin + warp, stride = alone ? 1 : kWarps;
   const int mine = turn < end ? static_cast<int>((end - turn + stride - 1) / stride) : 0;
   bool dead = false;  // a wait ran out: nothing is issued or awaited after
+  // lane i holds strip i % 2 of pair i / 2 of the round of 16 pairs that is being issued; of the
+  // round before, its rows
+  uint64_t here = 0;
+  int before = 0;
+  unsigned filled = 0;
   const auto issue = [&](int n) {  // the warp's n-th pair into stage n % 2, which is free
     if (n >= mine) return;
-    if ((n & 15) == 0) {  // lane i finds strip i % 2 of pair n + i / 2
+    if ((n & 15) == 0) {
+      before = static_cast<int>(here >> 48);
+      here = 0;
       const int i = n + lane / 2;
-      uint64_t e = 0;
       if (i < mine) {
         const uint32_t at = turn + uint32_t(i) * stride;
         const At p = place(at);
         const int v = 2 * static_cast<int>(at - p.u0) + (lane & 1);
         const UnitMap map = unit_map(a, a.lens[p.r]);
-        if (v < map.total()) e = locate(a, map, p.r, p.h, v, SB);
+        if (v < map.total()) here = locate(a, map, p.r, p.h, v, SB);
       }
-      where[(2 * n + lane) & 63] = e;
-      __syncwarp();
+      filled = __ballot_sync(0xffffffffu, here != 0);
     }
-    if (lane < 2) {
-      const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(where + ((2 * n) & 63));
+    if (lane / 2 == (n & 15)) {
       uint64_t* bar = bars + n % kStages;
-      if (lane == 0) mbar_arrive_tx(bar, SB * ((e.x != 0) + (e.y != 0)));
-      const uint64_t x = lane == 0 ? e.x : e.y;
-      if (x != 0)
-        bulk_g2s(ring + ((n % kStages) * 2 + lane) * SB, a.pool + (x & 0xffffffffffffull), SB, bar);
+      if ((lane & 1) == 0) mbar_arrive_tx(bar, SB * __popc((filled >> lane) & 3u));
+      if (here != 0)
+        bulk_g2s(ring + ((n % kStages) * 2 + (lane & 1)) * SB, a.pool + (here & 0xffffffffffffull),
+                 SB, bar);
     }
   };
   uint32_t* qw = reinterpret_cast<uint32_t*>(
@@ -648,8 +653,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     __syncthreads();
   }
 
-  int j = 0;  // the warp's next pair
-  for (uint32_t at = begin; at < end;) {
+  int j = 0;      // the warp's next pair
+  int later = 0;  // not the worker's first unit
+  for (uint32_t at = begin; at < end; later = 1) {
     uint32_t stop;
     {
       const At p = place(at);
@@ -703,8 +709,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
           continue;
         }
       }
-      const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(where + ((2 * j) & 63));
-      const int v0 = static_cast<int>(e.x >> 48), v1 = static_cast<int>(e.y >> 48);
+      // (pair j + 1 was issued last: in j's round or the next)
+      const int rows = (j & 15) == 15 && j + 1 < mine ? before : static_cast<int>(here >> 48);
+      const int v0 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15));
+      const int v1 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15) + 1);
       if (v0 | v1)
         pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + (j % kStages) * 2 * SB), v0,
                                  v1, qw, fac, st);
@@ -738,15 +746,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     const At p = place(at);  // (again: nothing of it is kept over the loop)
     const bool whole = at == p.u0 && stop == p.u0 + p.n;
     const int64_t row0 = (int64_t(p.r) * a.heads + p.h) * a.group + p.h0;
-    float* part = a.parts + (int64_t(worker) * 2 + (at == begin ? 0 : 1)) * S::kSlot;
+    float* part = a.parts + (int64_t(worker) * 2 + later) * S::kSlot;
     float* to = alone ? part : slots + warp * S::kSlot;
     if (at == p.u0 && lane == 0 && (alone || warp == 0)) {
       // this worker holds the unit's first pair; the last one's holds its last
       const uint32_t x0 = cost_at(p);
       a.units[int64_t(p.r) * units + p.u] =
           whole ? make_int2(0, 1)
-                : make_int2(static_cast<int>(worker) * 2 + (at == begin ? 0 : 1),
-                            static_cast<int>((x0 + p.n - 1) / chunk - x0 / chunk) + 1);
+                : make_int2(static_cast<int>(worker) * 2 + later,
+                            static_cast<int>((x0 + p.n - 1) / s_chunk - x0 / s_chunk) + 1);
     }
     if (!(alone && whole)) {
 #pragma unroll
