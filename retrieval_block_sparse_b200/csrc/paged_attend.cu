@@ -79,6 +79,7 @@ struct PagedAttendArgs {
   int chunks;         // head chunks of a kv head
   int first;          // sink / bs
   int whole;          // workers take whole units
+  bool q_vec;         // rows of q start on a boundary of four elements
   FastDiv by_bs, by_strips, by_units, by_chunks;
 };
 
@@ -421,10 +422,7 @@ __device__ __forceinline__ void load_q(const PagedAttendArgs& a, const T* q, boo
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] = 0.f;
-  if (live && lane * 4 < a.dim) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = Elem<T>::to_f32(q[lane * 4 + e]);
-  }
+  if (live && lane * 4 < a.dim) load4(q + lane * 4, a.q_vec, x);
 }
 template <int P, bool kWide, bool kLo>
 __device__ __forceinline__ void stage_q(const PagedAttendArgs& a, const float* x, int hh,
@@ -549,20 +547,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       max((cost + workers - 1) / workers,
           min(longest, static_cast<uint32_t>(alone ? kAloneLeast : kTeamLeast)) + extra);
   if (lane == 0) s_chunk = chunk;  // (every warp the same value: its own lanes read it back)
-  if (!a.whole && uint64_t(chunk) * worker >= cost) return;
 
-  const auto place = [&](uint32_t at) {  // of a pair
+  const auto at_unit = [&](int r, uint32_t u) {
     At p;
-    p.r = last_at_most(pre, a.R, div(static_cast<int>(at), a.by_units));
-    p.n = pre[p.r + 1] - pre[p.r];
-    const uint32_t base = uint32_t(pre[p.r]) * units;
-    p.u = (at - base) / p.n;
-    p.u0 = base + p.u * p.n;
-    p.h = div(static_cast<int>(p.u), a.by_chunks);
-    p.h0 = (static_cast<int>(p.u) - p.h * a.chunks) * H;
+    p.r = r;
+    p.n = pre[r + 1] - pre[r];
+    p.u = u;
+    p.u0 = uint32_t(pre[r]) * units + u * p.n;
+    p.h = div(static_cast<int>(u), a.by_chunks);
+    p.h0 = (static_cast<int>(u) - p.h * a.chunks) * H;
     p.nh = min(H, a.group - p.h0);
     return p;
   };
+  const auto place = [&](uint32_t at) {  // of a pair
+    const int r = last_at_most(pre, a.R, div(static_cast<int>(at), a.by_units));
+    return at_unit(r, (at - uint32_t(pre[r]) * units) / uint32_t(pre[r + 1] - pre[r]));
+  };
+  const auto unit_no = [&](const At& p) { return cnt[p.r] * units + p.u; };
   const auto cost_at = [&](const At& p) {  // of a unit's first pair
     return (uint32_t(pre[p.r]) + extra * cnt[p.r]) * units + p.u * (p.n + extra);
   };
@@ -580,8 +581,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     const uint32_t u = in / (n + extra);
     return uint32_t(pre[lo]) * units + u * n + min(in - u * (n + extra), n);
   };
-  const auto unit_at = [&](uint32_t i) {  // the first pair of the line's i-th unit
-    if (i >= some * units) return all;
+  const auto unit_of = [&](uint32_t i) {  // the line's i-th unit
     const uint32_t k = div(static_cast<int>(i), a.by_units);
     int lo = 0, hi = a.R;
     while (hi - lo > 1) {
@@ -589,17 +589,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       if (cnt[mid] <= k) lo = mid;
       else hi = mid;
     }
-    return uint32_t(pre[lo]) * units + (i - k * units) * uint32_t(pre[lo + 1] - pre[lo]);
+    return at_unit(lo, i - k * units);
   };
-  uint32_t begin, end;
-  if (a.whole) {
-    begin = unit_at(static_cast<uint32_t>(uint64_t(some) * units * worker / workers));
-    end = unit_at(static_cast<uint32_t>(uint64_t(some) * units * (worker + 1) / workers));
-  } else {
-    begin = pair_at(chunk * worker);
-    end = uint64_t(chunk) * (worker + 1) >= cost ? all : pair_at(chunk * (worker + 1));
+  // the worker's pairs, and its CTA's: lane i finds the i-th bound
+  uint32_t begin, end, cta_begin, cta_end;
+  {
+    const uint32_t w = lane < 2 ? worker + lane
+                       : alone  ? blockIdx.x * kWarps + (lane & 1) * kWarps : worker + (lane & 1);
+    uint32_t x = all;
+    if (a.whole) {
+      const uint32_t i = static_cast<uint32_t>(uint64_t(some) * units * w / workers);
+      if (i < some * units) x = unit_of(i).u0;
+    } else if (uint64_t(chunk) * w < cost) {
+      x = pair_at(chunk * w);
+    }
+    begin = __shfl_sync(0xffffffffu, x, 0);
+    end = __shfl_sync(0xffffffffu, x, 1);
+    cta_begin = __shfl_sync(0xffffffffu, x, 2);
+    cta_end = __shfl_sync(0xffffffffu, x, 3);
   }
-  if (begin >= end) return;  // (no pair among what it was dealt)
+  if (cta_begin >= cta_end) return;  // (no pair among what it was dealt)
 
   // the warp's pairs: begin + warp, + 8, .. of the CTA's, or all of its own
   const uint32_t turn = alone ? begin : begin + warp, stride = alone ? 1 : kWarps;
@@ -633,53 +642,69 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
                  SB, bar);
     }
   };
-  uint32_t* qw = reinterpret_cast<uint32_t*>(
-      alone ? sm + S::kSlots + warp * S::kSlot * 4 : sm + S::kQ);
-  float* s_fac = reinterpret_cast<float*>(sm + S::kFac) + (alone ? warp * 8 : 0);
+  // q operands: one for the CTA, or a place for each of the units in its warps' lines (for each of
+  // its warps, where there are more units)
+  const auto q_place = [&](int i) {
+    return reinterpret_cast<uint32_t*>(alone ? sm + S::kSlots + i * S::kSlot * 4 : sm + S::kQ);
+  };
+  const auto fac_place = [&](int i) { return reinterpret_cast<float*>(sm + S::kFac) + 8 * i; };
   const auto fetch = [&](const At& p, int hh, float* x) {
     load_q(a, static_cast<const T*>(a.q) + p.r * a.q_req +
                   (int64_t(p.h) * a.group + p.h0 + hh) * a.q_head, hh < p.nh, x);
   };
-  const auto stage = [&](const At& p, int hh) {
+  const auto stage = [&](const At& p, int hh) {  // one head of a CTA's unit
     float x[4];
     fetch(p, hh, x);
-    stage_q<P, kWide, kLo>(a, x, hh, qw, s_fac);
+    stage_q<P, kWide, kLo>(a, x, hh, q_place(0), fac_place(0));
+  };
+  const auto stage_all = [&](const At& p, int i) {  // a unit's heads into place i
+    float x[H][4];
+#pragma unroll
+    for (int hh = 0; hh < H; ++hh) fetch(p, hh, x[hh]);
+#pragma unroll
+    for (int hh = 0; hh < H; ++hh) {
+      if (hh < p.nh) stage_q<P, kWide, kLo>(a, x[hh], hh, q_place(i), fac_place(i));
+      else zero_q<P, kWide, kLo>(hh, q_place(i), fac_place(i));
+    }
   };
 
 #pragma unroll 1
   for (int n = 0; n < kStages; ++n) issue(n);
-  if (!alone) {
-    if (warp < H) stage(place(begin), warp);
-    __syncthreads();
+  uint32_t first_unit = 0;
+  bool shared_q = !alone;
+  if (alone) {
+    first_unit = unit_no(place(cta_begin));
+    const uint32_t n = unit_no(place(cta_end - 1)) - first_unit + 1;
+    shared_q = n <= kWarps;
+    if (shared_q && warp < static_cast<int>(n)) stage_all(unit_of(first_unit + warp), warp);
+  } else if (warp < H) {
+    stage(place(begin), warp);
   }
+  if (shared_q) __syncthreads();
 
   int j = 0;      // the warp's next pair
   int later = 0;  // not the worker's first unit
   for (uint32_t at = begin; at < end; later = 1) {
     uint32_t stop;
+    int at_place;
     {
       const At p = place(at);
       stop = min(end, p.u0 + p.n);
-      if (alone) {
-        float x[H][4];
-#pragma unroll
-        for (int hh = 0; hh < H; ++hh) fetch(p, hh, x[hh]);
+      at_place = !alone ? 0 : shared_q ? static_cast<int>(unit_no(p) - first_unit) : warp;
+      if (!shared_q) {
         __syncwarp();
-#pragma unroll
-        for (int hh = 0; hh < H; ++hh) {
-          if (hh < p.nh) stage_q<P, kWide, kLo>(a, x[hh], hh, qw, s_fac);
-          else zero_q<P, kWide, kLo>(hh, qw, s_fac);
-        }
+        stage_all(p, warp);
         __syncwarp();
       }
     }
+    const uint32_t* qw = q_place(at_place);
     float fac[HL];
     State<P, kWide> st;
     st.e = kMostE;
     st.most = pow2(kScaleTop - kMostE);
 #pragma unroll
     for (int i = 0; i < HL; ++i) {
-      fac[i] = s_fac[HL * (lane & 3) + i];
+      fac[i] = fac_place(at_place)[HL * (lane & 3) + i];
       st.m[i] = st.top[i] = -INFINITY;
       st.l[i] = 0.f;
     }
@@ -971,6 +996,8 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
   a.sink = sink;
   a.window = window;
   a.chunks = chunks_of(s);
+  a.q_vec = reinterpret_cast<uintptr_t>(q) % (4 * dtype_size(s->d.dtype)) == 0 &&
+            ((q_request_stride | q_head_stride) & 3) == 0;
   a.first = sink / a.bs;
   // the longest unit there can be: what sink, selection and window ask for, or the whole table
   const int64_t strips = std::min<int64_t>(

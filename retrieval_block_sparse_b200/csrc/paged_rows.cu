@@ -33,28 +33,6 @@ struct RowArgs {
   bool vec;    // every row starts on a boundary of four elements
 };
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, bool vec, float* x);
-template <>
-__device__ __forceinline__ void load4(const float* p, bool vec, float* x) {
-  if (vec) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-  } else {
-    x[0] = p[0]; x[1] = p[1]; x[2] = p[2]; x[3] = p[3];
-  }
-}
-template <>
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, bool vec, float* x) {
-  if (vec) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xffff0000u);
-    x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __bfloat162float(p[i]);
-  }
-}
 __device__ __forceinline__ void store4(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }

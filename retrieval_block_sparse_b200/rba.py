@@ -604,21 +604,22 @@ class PagedStore:
             self._refuse("workspace", t, tuple(t.shape), torch.uint8)
         return t.data_ptr(), t.numel()
 
-    def _new(self, shape, dt):
-        return torch.empty(shape, dtype=dt, device=self.device)
+    def _out(self, name, t, shape, dt):
+        """(t, pointer) of an output: the caller's, checked, or a new one."""
+        if t is None:
+            t = self.lens.new_empty(shape, dtype=dt)  # (cheaper on the host than torch.empty)
+            return t, t.data_ptr()
+        return t, self._arg(name, t, shape, dt)
 
     # -- page tables -------------------------------------------------------------
     def extend(self, n_new, n_slots, *, slots=None, starts=None):
         """Grows request r by n_new[r] tokens.  Returns (slots [n_slots], -1 past the new
         tokens; starts [R + 1], the first new token of each request)."""
         R = n_new.shape[0]
-        if slots is None:
-            slots = self._new((n_slots,), torch.int32)
-        if starts is None:
-            starts = self._new((R + 1,), torch.int32)
-        self._call("rba_paged_extend", self._arg("n_new", n_new, (R,), torch.int32), R,
-                   self._arg("slots", slots, (n_slots,), torch.int32), n_slots,
-                   self._arg("starts", starts, (R + 1,), torch.int32))
+        slots, sp = self._out("slots", slots, (n_slots,), torch.int32)
+        starts, tp = self._out("starts", starts, (R + 1,), torch.int32)
+        self._call("rba_paged_extend", self._arg("n_new", n_new, (R,), torch.int32), R, sp, n_slots,
+                   tp)
         return slots, starts
 
     def truncate(self, keep):
@@ -640,12 +641,9 @@ class PagedStore:
         """Rows at the slots as the values held there: (k, v), each [n][Hkv][D]."""
         n = slots.shape[0]
         shape = (n, self.Hkv, self.D)
-        if k is None:
-            k = self._new(shape, self._td)
-        if v is None:
-            v = self._new(shape, self._td)
-        self._call("rba_paged_read", self._arg("slots", slots, (n,), torch.int32), n,
-                   self._arg("k", k, shape, self._td), self._arg("v", v, shape, self._td))
+        k, kp = self._out("k", k, shape, self._td)
+        v, vp = self._out("v", v, shape, self._td)
+        self._call("rba_paged_read", self._arg("slots", slots, (n,), torch.int32), n, kp, vp)
         return k, v
 
     # -- select, attend --------------------------------------------------------------
@@ -658,12 +656,10 @@ class PagedStore:
         ascending, -1 past a request's candidates."""
         R = q.shape[0]
         qp, qr, qh = self._rows("q", q, R, self.Hq)
-        if idx is None:
-            idx = self._new((R, self.Hkv, k), torch.int32)
+        idx, ip = self._out("idx", idx, (R, self.Hkv, k), torch.int32)
         if workspace is None:
             workspace = self.select_workspace()
-        self._call("rba_paged_select", qp, qr, qh, R, k, sink, window,
-                   self._arg("idx", idx, (R, self.Hkv, k), torch.int32), *self._bytes(workspace))
+        self._call("rba_paged_select", qp, qr, qh, R, k, sink, window, ip, *self._bytes(workspace))
         return idx
 
     def attend_workspace(self):
@@ -681,15 +677,12 @@ class PagedStore:
         ip = self._arg("idx", idx, (R, self.Hkv, k), torch.int32) if k else None
         if scale is None:
             scale = 1.0 / math.sqrt(self.D)
-        if out is None:
-            out = self._new((R, self.Hq, self.D), torch.float32)
-        if lse is None:
-            lse = self._new((R, self.Hq), torch.float32)
+        out, op = self._out("out", out, (R, self.Hq, self.D), torch.float32)
+        lse, lp = self._out("lse", lse, (R, self.Hq), torch.float32)
         if workspace is None:
             workspace = self.attend_workspace()
-        self._call("rba_paged_attend", qp, qr, qh, R, ip, k, sink, window, scale,
-                   self._arg("out", out, (R, self.Hq, self.D), torch.float32),
-                   self._arg("lse", lse, (R, self.Hq), torch.float32), *self._bytes(workspace))
+        self._call("rba_paged_attend", qp, qr, qh, R, ip, k, sink, window, scale, op, lp,
+                   *self._bytes(workspace))
         return out, lse
 
     def check(self):
