@@ -46,7 +46,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 2;  // pairs of strips in a warp's ring
+constexpr int kStages = 2;  // pairs of strips in a warp's ring (pair n takes place n % 2)
 // What a unit's start and end cost, in pairs of its worker, and the pairs that a worker takes at
 // least (or a whole unit): for CTAs and for single warps.
 constexpr int kTeamCost = 10, kAloneCost = 3;
@@ -150,11 +150,11 @@ __device__ __forceinline__ UnitMap unit_map(const PagedAttendArgs& a, int T) {
   return m;
 }
 
-// Strip v of a unit as a table entry: its byte offset in the pool, and its valid rows [ra, rb) as
-// (ra + 32 rb) << 48 (0: nothing of it is attended to).
-constexpr int kWholeStrip = 32 * kStrip;
-__device__ __forceinline__ uint64_t locate(const PagedAttendArgs& a, const UnitMap& m, int r,
-                                           int h, int v, int sbytes) {
+// Strip v of a unit: its address, and its valid rows [ra, rb) as ra + 32 rb (0: nothing of it is
+// attended to).
+constexpr int kWholeStrip = 32 * kStrip, kWholePair = kWholeStrip << 16 | kWholeStrip;
+__device__ __forceinline__ const uint8_t* locate(const PagedAttendArgs& a, const UnitMap& m, int r,
+                                                 int h, int v, int sbytes, int* valid) {
   int lin, lo, hi;
   if (v < m.ns) {
     lin = v;
@@ -165,7 +165,7 @@ __device__ __forceinline__ uint64_t locate(const PagedAttendArgs& a, const UnitM
     const int j = a.idx[(int64_t(r) * a.heads + h) * a.k + i];
     if (j < m.g.first || j >= m.g.first + m.g.nc) {
       report(a.status, RBA_ERR_BOUNDS, kWherePaged, j);
-      return 0;
+      return a.pool;
     }
     lin = j * a.strips + (v - m.ns) - i * a.strips;
     lo = m.g.sink_end;
@@ -179,14 +179,13 @@ __device__ __forceinline__ uint64_t locate(const PagedAttendArgs& a, const UnitM
   const int page = a.table[int64_t(r) * a.max_pages + j];
   if (page < 0 || page >= a.n_pages) {
     report(a.status, RBA_ERR_BOUNDS, kWherePaged, page);
-    return 0;
+    return a.pool;
   }
   const int pos0 = j * a.bs + sp * kStrip;
   const int ra = max(lo - pos0, 0);
   const int rb = min(min(kStrip, hi - pos0), a.bs - sp * kStrip);
-  if (rb <= ra) return 0;
-  return uint64_t((int64_t(page) * a.heads + h) * a.strips + sp) * sbytes |
-         uint64_t(ra + 32 * rb) << 48;
+  if (rb > ra) *valid = ra + 32 * rb;
+  return a.pool + ((int64_t(page) * a.heads + h) * a.strips + sp) * sbytes;
 }
 
 // The same for one byte of each half word (0: the low ones): the codes of its low nibbles, and
@@ -241,12 +240,12 @@ template <int P, bool kWide> struct State {
 };
 
 template <int P, bool kWide, bool kLo>
-__device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int valid1,
+__device__ __forceinline__ void pair_step(const uint8_t* strips, int valid2,
                                           const uint32_t* qw, const float* fac,
                                           State<P, kWide>& st) {
   constexpr int G = P / 32, HL = kWide ? 2 : 1, SB = strip_bytes(P);
   const int lane = threadIdx.x & 31, t = lane >> 2;
-  const bool whole = valid0 == kWholeStrip && valid1 == kWholeStrip;
+  const bool whole = valid2 == kWholePair;
   float y[HL][2][2];        // logits of tokens t and t + 8 of each strip for the lane's heads
   uint32_t sv[2][2][G / 2]; // their V scales, two to a word
 #pragma unroll
@@ -293,7 +292,7 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid0, int
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int valid = n == 0 ? valid0 : valid1;
+        const int valid = n == 0 ? valid2 & 0xffff : valid2 >> 16;
         if (t + 8 * half >= (valid & 31) && t + 8 * half < (valid >> 5)) continue;
 #pragma unroll
         for (int i = 0; i < G / 2; ++i) sv[n][half][i] = 0;
@@ -612,34 +611,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
 
   // the warp's pairs: begin + warp, + 8, .. of the CTA's, or all of its own
   const uint32_t turn = alone ? begin : begin + warp, stride = alone ? 1 : kWarps;
-  const int mine = turn < end ? static_cast<int>((end - turn + stride - 1) / stride) : 0;
-  bool dead = false;  // a wait ran out: nothing is issued or awaited after
-  // lane i holds strip i % 2 of pair i / 2 of the round of 16 pairs that is being issued; of the
-  // round before, its rows
-  uint64_t here = 0;
-  int before = 0;
-  unsigned filled = 0;
+  const auto pairs_below = [&](uint32_t x) {  // how many of them lie before pair x of the line
+    return x <= turn ? 0 : static_cast<int>(alone ? x - turn : (x - turn + kWarps - 1) / kWarps);
+  };
+  int mine = pairs_below(end);
+  // lanes 2 i and 2 i + 1 hold the strips of pair i of the round of 16 pairs that is being issued:
+  // the lane's strip, and both strips' rows (rows0 | rows1 << 16); of the round before, those rows
+  const uint8_t* src = a.pool;
+  int rows = 0, rows_before = 0;
+  const auto find = [&](int n) {
+    rows_before = rows;
+    int valid = 0;
+    const int i = n + lane / 2;
+    if (i < mine) {
+      const uint32_t at = turn + uint32_t(i) * stride;
+      const At p = place(at);
+      const int v = 2 * static_cast<int>(at - p.u0) + (lane & 1);
+      const UnitMap map = unit_map(a, a.lens[p.r]);
+      if (v < map.total()) src = locate(a, map, p.r, p.h, v, SB, &valid);
+    }
+    const int other = __shfl_xor_sync(0xffffffffu, valid, 1);
+    rows = lane & 1 ? other | valid << 16 : valid | other << 16;
+  };
   const auto issue = [&](int n) {  // the warp's n-th pair into stage n % 2, which is free
     if (n >= mine) return;
-    if ((n & 15) == 0) {
-      before = static_cast<int>(here >> 48);
-      here = 0;
-      const int i = n + lane / 2;
-      if (i < mine) {
-        const uint32_t at = turn + uint32_t(i) * stride;
-        const At p = place(at);
-        const int v = 2 * static_cast<int>(at - p.u0) + (lane & 1);
-        const UnitMap map = unit_map(a, a.lens[p.r]);
-        if (v < map.total()) here = locate(a, map, p.r, p.h, v, SB);
-      }
-      filled = __ballot_sync(0xffffffffu, here != 0);
-    }
+    if ((n & 15) == 0) find(n);
     if (lane / 2 == (n & 15)) {
-      uint64_t* bar = bars + n % kStages;
-      if ((lane & 1) == 0) mbar_arrive_tx(bar, SB * __popc((filled >> lane) & 3u));
-      if (here != 0)
-        bulk_g2s(ring + ((n % kStages) * 2 + (lane & 1)) * SB, a.pool + (here & 0xffffffffffffull),
-                 SB, bar);
+      uint64_t* bar = bars + (n & 1);
+      if ((lane & 1) == 0) mbar_arrive_tx(bar, ((rows & 0xffff) ? SB : 0) + (rows >> 16 ? SB : 0));
+      if (lane & 1 ? rows >> 16 : rows & 0xffff)
+        bulk_g2s(ring + ((n & 1) * 2 + (lane & 1)) * SB, src, SB, bar);
     }
   };
   // q operands: one for the CTA, or a place for each of the units in its warps' lines (for each of
@@ -713,11 +714,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.acc[b][i] = 0.f;
 
+    int till = min(mine, pairs_below(stop));
 #pragma unroll 1
-    for (; j < mine && turn + uint32_t(j) * stride < stop; ++j) {
-      if (dead) continue;
-      const uint32_t parity = (j / kStages) & 1;
-      uint64_t* bar = bars + j % kStages;
+    for (; j < till; ++j) {
+      uint64_t* bar = bars + (j & 1);
+      const uint32_t parity = (j >> 1) & 1;
       bool ok = mbar_try(bar, parity);
       if (!__all_sync(0xffffffffu, ok)) {
         const unsigned long long t0 = now_ns();
@@ -729,18 +730,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
           if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, j);
           // copies in flight land before the warp goes on without its pairs
           mbar_drain(bar, parity);
-          if (j + 1 < mine) mbar_drain(bars + (j + 1) % kStages, ((j + 1) / kStages) & 1);
-          dead = true;
-          continue;
+          if (j + 1 < mine) mbar_drain(bars + (~j & 1), ((j + 1) >> 1) & 1);
+          mine = till = 0;
+          break;
         }
       }
       // (pair j + 1 was issued last: in j's round or the next)
-      const int rows = (j & 15) == 15 && j + 1 < mine ? before : static_cast<int>(here >> 48);
-      const int v0 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15));
-      const int v1 = __shfl_sync(0xffffffffu, rows, 2 * (j & 15) + 1);
-      if (v0 | v1)
-        pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + (j % kStages) * 2 * SB), v0,
-                                 v1, qw, fac, st);
+      const int r2 = __shfl_sync(0xffffffffu, (j & 15) == 15 && j + 1 < mine ? rows_before : rows,
+                                 2 * (j & 15));
+      if (r2 != 0)
+        pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + (j & 1) * 2 * SB), r2, qw,
+                                 fac, st);
       __syncwarp();
       issue(j + kStages);
     }
