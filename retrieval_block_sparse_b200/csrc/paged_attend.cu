@@ -106,6 +106,28 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// Whether the barrier's phase is over, for the whole warp (shared-memory address).
+__device__ __forceinline__ bool phase_over(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " vote.sync.all.pred p, p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+// Arms the barrier with `bytes` where `arm`, and copies `bytes1` to dst where they are not 0
+// (predicated: no branch).
+__device__ __forceinline__ void arm_and_copy(uint32_t bar, int arm, uint32_t bytes, uint32_t dst,
+                                             const void* src, uint32_t bytes1) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %0, 0;\n setp.ne.u32 q, %4, 0;\n"
+      " @p mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%1], %2;\n"
+      " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%3], [%5], %4, [%1];\n"
+      "}\n" ::"r"(arm), "r"(bar), "r"(bytes), "r"(dst), "r"(bytes1), "l"(src)
+      : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -616,9 +638,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   };
   int mine = pairs_below(end);
   // lanes 2 i and 2 i + 1 hold the strips of pair i of the round of 16 pairs that is being issued:
-  // the lane's strip, and both strips' rows (rows0 | rows1 << 16); of the round before, those rows
+  // the lane's strip and its bytes, and both strips' rows (rows0 | rows1 << 16); of the round
+  // before, those rows
   const uint8_t* src = a.pool;
+  uint32_t bytes = 0, bytes_both = 0;
   int rows = 0, rows_before = 0;
+  const uint32_t bar0 = smem_u32(bars), place0 = smem_u32(ring) + (lane & 1) * SB;
   const auto find = [&](int n) {
     rows_before = rows;
     int valid = 0;
@@ -631,17 +656,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       if (v < map.total()) src = locate(a, map, p.r, p.h, v, SB, &valid);
     }
     const int other = __shfl_xor_sync(0xffffffffu, valid, 1);
+    bytes = valid ? SB : 0;
+    bytes_both = bytes + (other ? SB : 0);
     rows = lane & 1 ? other | valid << 16 : valid | other << 16;
   };
   const auto issue = [&](int n) {  // the warp's n-th pair into stage n % 2, which is free
     if (n >= mine) return;
     if ((n & 15) == 0) find(n);
-    if (lane / 2 == (n & 15)) {
-      uint64_t* bar = bars + (n & 1);
-      if ((lane & 1) == 0) mbar_arrive_tx(bar, ((rows & 0xffff) ? SB : 0) + (rows >> 16 ? SB : 0));
-      if (lane & 1 ? rows >> 16 : rows & 0xffff)
-        bulk_g2s(ring + ((n & 1) * 2 + (lane & 1)) * SB, src, SB, bar);
-    }
+    const bool me = lane / 2 == (n & 15);
+    arm_and_copy(bar0 + (n & 1) * 8, me && (lane & 1) == 0, bytes_both, place0 + (n & 1) * 2 * SB,
+                 src, me ? bytes : 0);
   };
   // q operands: one for the CTA, or a place for each of the units in its warps' lines (for each of
   // its warps, where there are more units)
@@ -717,19 +741,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     int till = min(mine, pairs_below(stop));
 #pragma unroll 1
     for (; j < till; ++j) {
-      uint64_t* bar = bars + (j & 1);
-      const uint32_t parity = (j >> 1) & 1;
-      bool ok = mbar_try(bar, parity);
-      if (!__all_sync(0xffffffffu, ok)) {
+      const uint32_t bar = bar0 + (j & 1) * 8, parity = (j >> 1) & 1;
+      if (!phase_over(bar, parity)) {
         const unsigned long long t0 = now_ns();
+        bool over, late;
         do {
-          if (!ok) ok = mbar_try(bar, parity);
-        } while (!__all_sync(0xffffffffu, ok) &&
-                 !__shfl_sync(0xffffffffu, now_ns() - t0 > kTimeoutNs, 0));
-        if (!__all_sync(0xffffffffu, ok)) {
+          over = phase_over(bar, parity);
+          late = __shfl_sync(0xffffffffu, now_ns() - t0 > kTimeoutNs, 0);
+        } while (!over && !late);
+        if (!over) {
           if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, j);
           // copies in flight land before the warp goes on without its pairs
-          mbar_drain(bar, parity);
+          mbar_drain(bars + (j & 1), parity);
           if (j + 1 < mine) mbar_drain(bars + (~j & 1), ((j + 1) >> 1) & 1);
           mine = till = 0;
           break;
