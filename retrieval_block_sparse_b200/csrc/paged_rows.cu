@@ -13,8 +13,6 @@
 namespace rba {
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
 constexpr float kLeastScale = 0x1p-100f;
 constexpr float kToInt = 12582920.f;  // 1.5 2^23 + 8: adding it leaves rint(x) + 8 in the low bits
 
@@ -29,10 +27,47 @@ struct RowArgs {
   float* rep;
   int32_t* status;
   int n, heads, dim, bs, strips, n_pages;
-  int window;  // slots a warp looks for strips in
+  int window;  // slots a CTA looks for runs in
+  FastDiv by_bs, by_heads;
   bool vec;    // every row starts on a boundary of four elements
 };
 
+// Four elements of a row as they were loaded: their values, and the bits of the largest |x|
+// (compared as integers: values that are not finite are the largest).
+template <typename T> struct Four;
+template <> struct Four<float> {
+  float x[4];
+  __device__ __forceinline__ void load(const float* p, bool vec) { load4(p, vec, x); }
+  __device__ __forceinline__ void zero() { x[0] = x[1] = x[2] = x[3] = 0.f; }
+  __device__ __forceinline__ float operator[](int i) const { return x[i]; }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+  }
+};
+template <> struct Four<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool vec) {
+    if (vec) {
+      u = *reinterpret_cast<const uint2*>(p);
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      u.x = h[0] | uint32_t(h[1]) << 16;
+      u.y = h[2] | uint32_t(h[3]) << 16;
+    }
+  }
+  __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = i < 2 ? u.x : u.y;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu);
+    return max(m << 16, m & 0xffff0000u);
+  }
+};
 __device__ __forceinline__ void store4(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
@@ -54,7 +89,8 @@ __device__ __forceinline__ void scale_of_max(uint32_t bits, uint16_t* scale, flo
   *inv = odd || none ? 0.f : __frcp_rn(sf);
 }
 // Four codes, one 16-bit unit.  |x| inv <= 7 (1 + 2^-8) rounds to 7 at most: no clamp is needed.
-__device__ __forceinline__ uint32_t unit_of(const float* x, float inv) {
+template <typename R>
+__device__ __forceinline__ uint32_t unit_of(const R& x, float inv) {
   uint32_t b[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[j], inv), kToInt));
@@ -78,7 +114,7 @@ __device__ __forceinline__ void values4(uint32_t unit, float s, float* x) {
 // are computed once per group.  Everything goes to `to`, the strip or its copy in shared memory;
 // v_pairs: the tokens' V units can be written two at a time.
 template <typename T, int P>
-__device__ __forceinline__ void write_half(const RowArgs& a, int i0, int h, int t0, int n,
+__device__ __forceinline__ void write_half(const RowArgs& a, int64_t i0, int h, int t0, int n,
                                            int which, int half, uint8_t* to, bool v_pairs) {
   constexpr int LPR = P / 4;
   const int lane = threadIdx.x & 31, sub = lane % LPR, g = sub / 8, l = sub % 8;
@@ -87,20 +123,17 @@ __device__ __forceinline__ void write_half(const RowArgs& a, int i0, int h, int 
   const T* base = which == 0 ? static_cast<const T*>(a.k) + i0 * a.k_tok + h * a.k_head
                              : static_cast<const T*>(a.v) + i0 * a.v_tok + h * a.v_head;
   const int64_t step = which == 0 ? a.k_tok : a.v_tok;
-  float x[8][4];
+  Four<T> x[8];
+  const T* p = base + first * step + sub * 4;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
+  for (int j = 0; j < 8; ++j, p += step) {
     const int i = first + j;
-    if (i >= 0 && i < n && sub * 4 < a.dim) load4(base + i * step + sub * 4, a.vec, x[j]);
+    if (i >= 0 && i < n && sub * 4 < a.dim) x[j].load(p, a.vec);
+    else x[j].zero();
   }
   uint32_t m[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    m[j] = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m[j] = max(m[j], __float_as_uint(x[j][e]) & 0x7fffffffu);
-  }
+  for (int j = 0; j < 8; ++j) m[j] = x[j].top();
   // halving: after the step of width w a lane keeps the w rows that share its bit w
 #pragma unroll
   for (int w = 4; w > 0; w >>= 1) {
@@ -137,29 +170,21 @@ __device__ __forceinline__ void write_half(const RowArgs& a, int i0, int h, int 
   }
 }
 
-// One CTA per (window of slots, head): it writes the runs, each of consecutive slots of one
-// strip, whose first slot lies in its window, a warp to each half strip of K and of V.  A whole
-// strip is put together in shared memory and leaves it in 16-byte pieces; a part of one goes out
-// unit by unit (the rows beside it belong to other calls).
-template <int P> constexpr int append_warps() { return P == 128 ? 4 : 2; }
-template <typename T, int P>
-__global__ void __launch_bounds__(append_warps<P>() * 32) append_kernel(RowArgs a) {
-  constexpr int SB = strip_bytes(P), kThreads = append_warps<P>() * 32;
-  __shared__ __align__(16) uint8_t s_stage[SB];
-  wait_for_stream();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int which = P == 128 ? warp >> 1 : lane >> 4, half = warp & 1;
-  const int h = blockIdx.x % a.heads;
-  const int64_t base = int64_t(blockIdx.x / a.heads) * a.window;
+// The runs whose first slot lies in this CTA's window of slots, each of consecutive slots of one
+// strip: calls f(first slot's index, rows, strip, first row of the strip) for each, with every
+// thread of the CTA.
+template <int P, typename F>
+__device__ __forceinline__ void for_runs(const RowArgs& a, int h, int64_t base, const F& f) {
+  const int lane = threadIdx.x & 31;
   // lane i looks at slot base - 1 + i (window <= 16: a run's 16 slots stay within the warp)
   const int64_t i = base - 1 + lane;
   int slot = i >= 0 && i < a.n ? a.slots[i] : -1;
   int page = 0, row = 0;
   if (slot >= 0) {
-    page = slot / a.bs;
+    page = div(slot, a.by_bs);
     row = slot - page * a.bs;
     if (page >= a.n_pages) {
-      if (h == 0 && warp == 0 && lane >= 1 && lane <= a.window)
+      if (h == 0 && threadIdx.x < 32 && lane >= 1 && lane <= a.window)
         report(a.status, RBA_ERR_BOUNDS, kWherePaged, slot);
       slot = -1;
     }
@@ -169,45 +194,66 @@ __global__ void __launch_bounds__(append_warps<P>() * 32) append_kernel(RowArgs 
   const unsigned follows = __ballot_sync(0xffffffffu, next);
   unsigned firsts = __ballot_sync(0xffffffffu, slot >= 0 && !next && lane >= 1 && lane <= a.window);
   while (firsts) {
-    const int f = __ffs(firsts) - 1;
+    const int k = __ffs(firsts) - 1;
     firsts &= firsts - 1;
-    const int n = __ffs(~(follows >> (f + 1)));  // the first and those that follow it
-    const int p = __shfl_sync(0xffffffffu, page, f), r = __shfl_sync(0xffffffffu, row, f);
-    uint8_t* strip = a.pool + ((int64_t(p) * a.heads + h) * a.strips + r / kStrip) * SB;
+    const int n = __ffs(~(follows >> (k + 1)));  // the first and those that follow it
+    const int p = __shfl_sync(0xffffffffu, page, k), r = __shfl_sync(0xffffffffu, row, k);
+    f(base - 1 + k, n, a.pool + ((int64_t(p) * a.heads + h) * a.strips + r / kStrip) * strip_bytes(P),
+      r % kStrip);
+  }
+}
+
+// One CTA per (window of slots, head) writes the window's runs, a warp to each half strip of K and
+// of V.  A whole strip is put together in shared memory and leaves it in 16-byte pieces; a part of
+// one goes out unit by unit (the rows beside it belong to other calls).
+// (Eight bf16 rows fit 40 registers a thread, 48 warps an SM; 32-bit rows take 64.)
+template <int P> constexpr int run_warps() { return P == 128 ? 4 : 2; }
+template <typename T, int P>
+__global__ void __launch_bounds__(run_warps<P>() * 32,
+                                  (sizeof(T) == 2 ? 1536 : 1024) / (run_warps<P>() * 32))
+    append_kernel(RowArgs a) {
+  constexpr int SB = strip_bytes(P), kThreads = run_warps<P>() * 32;
+  __shared__ __align__(16) uint8_t s_stage[SB];
+  wait_for_stream();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int which = P == 128 ? warp >> 1 : lane >> 4, half = warp & 1;
+  const int w = div(blockIdx.x, a.by_heads), h = blockIdx.x - w * a.heads;
+  for_runs<P>(a, h, int64_t(w) * a.window, [&](int64_t i0, int n, uint8_t* strip, int t0) {
     const bool whole = n == kStrip;
-    write_half<T, P>(a, static_cast<int>(base) - 1 + f, h, r % kStrip, n, which, half,
-                     whole ? s_stage : strip, whole);
-    if (!whole) continue;
+    write_half<T, P>(a, i0, h, t0, n, which, half, whole ? s_stage : strip, whole);
+    if (!whole) return;
     __syncthreads();
     for (int o = threadIdx.x * 16; o < SB; o += kThreads * 16)
       *reinterpret_cast<uint4*>(strip + o) = *reinterpret_cast<const uint4*>(s_stage + o);
     __syncthreads();
-  }
+  });
 }
 
-// Means of the pages whose last row is among the slots: one CTA per 32 slots and eight heads, one
-// warp per head.  Lane (t, c) sums rows t, t + 8, .. over dims 8 c .. + 7 of each group in strip
-// order; halving exchanges add the eight lanes of a c and leave four dims with each.
+// Means of the pages whose last row is among the slots: one CTA per (32 slots, head), its warps
+// each a share of a page's strips.  Lane (t, c) sums rows t and t + 8 over dims 8 c .. + 7 of each
+// group; halving exchanges add the eight lanes of a c and leave G values with each; the warps' sums
+// are added in order.
+constexpr int kMeanWarps = 8;
 template <int P>
-__global__ void __launch_bounds__(kRowThreads) page_mean_kernel(RowArgs a) {
+__global__ void __launch_bounds__(kMeanWarps * 32) page_mean_kernel(RowArgs a) {
   constexpr int G = P / 32, SB = strip_bytes(P);
+  __shared__ float s_sum[kMeanWarps][P];
   wait_for_stream();
-  const int lane = threadIdx.x & 31, t = lane >> 2, c = lane & 3;
-  const int chunks = (a.heads + kRowWarps - 1) / kRowWarps;
-  const int h = blockIdx.x % chunks * kRowWarps + (threadIdx.x >> 5);
-  const int64_t i = int64_t(blockIdx.x / chunks) * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane >> 2, c = lane & 3;
+  const int w32 = div(blockIdx.x, a.by_heads), h = blockIdx.x - w32 * a.heads;
+  const int64_t i = int64_t(w32) * 32 + lane;
   const int mine = i < a.n ? a.slots[i] : -1;
+  const int at = mine >= 0 ? div(mine, a.by_bs) : 0;
   unsigned done = __ballot_sync(
-      0xffffffffu, mine >= 0 && mine / a.bs < a.n_pages && mine % a.bs == a.bs - 1);
-  if (h >= a.heads) return;
+      0xffffffffu, mine >= 0 && at < a.n_pages && mine - at * a.bs == a.bs - 1);
   for (; done; done &= done - 1) {
-    const int page = __shfl_sync(0xffffffffu, mine, __ffs(done) - 1) / a.bs;
-    const uint8_t* strip = a.pool + (int64_t(page) * a.heads + h) * a.strips * SB;
+    const int page = __shfl_sync(0xffffffffu, at, __ffs(done) - 1);
+    const uint8_t* strips = a.pool + (int64_t(page) * a.heads + h) * a.strips * SB;
     float acc[8 * G];
 #pragma unroll
     for (int e = 0; e < 8 * G; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < a.strips; ++s, strip += SB) {
+    for (int s = warp; s < a.strips; s += kMeanWarps) {
+      const uint8_t* strip = strips + int64_t(s) * SB;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t word[G];
@@ -226,7 +272,7 @@ __global__ void __launch_bounds__(kRowThreads) page_mean_kernel(RowArgs a) {
             acc[8 * g + j] = fmaf(code_of(word[g] >> (4 * j)), sc[g], acc[8 * g + j]);
       }
     }
-    // lane (t, c) ends with values (8 G / 8) t .. of the c's 8 G
+    // lane (t, c) ends with values G t .. of its c's 8 G
 #pragma unroll
     for (int w = 4; w > 0; w >>= 1) {
       const bool up = (t & w) != 0;
@@ -236,29 +282,37 @@ __global__ void __launch_bounds__(kRowThreads) page_mean_kernel(RowArgs a) {
         acc[e] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * w);
       }
     }
-    float* rep = a.rep + (int64_t(page) * a.heads + h) * P;
 #pragma unroll
     for (int e = 0; e < G; ++e) {
-      const int at = G * t + e;  // of (group, dim) = (at / 8, at % 8)
-      rep[32 * (at / 8) + 8 * c + at % 8] = acc[e] / static_cast<float>(a.bs);
+      const int v = G * t + e;  // of (group, dim) = (v / 8, v % 8)
+      s_sum[warp][32 * (v / 8) + 8 * c + v % 8] = acc[e];
     }
+    __syncthreads();
+    if (threadIdx.x < P) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMeanWarps; ++w) sum += s_sum[w][threadIdx.x];
+      a.rep[(int64_t(page) * a.heads + h) * P + threadIdx.x] = sum / static_cast<float>(a.bs);
+    }
+    __syncthreads();
   }
 }
 
-// One warp per slot and four heads: lane (g, l) four dims of a row (P = 64: K in one half of
+// One warp per slot and kHeads heads: lane (g, l) four dims of a row (P = 64: K in one half of
 // the warp, V in the other).
+constexpr int kReadWarps = 8, kHeads = 2;
 template <typename T, int P>
-__global__ void __launch_bounds__(kRowThreads) read_kernel(RowArgs a) {
-  constexpr int LPR = P / 4, SB = strip_bytes(P), kHeads = 4;
+__global__ void __launch_bounds__(kReadWarps * 32) read_kernel(RowArgs a) {
+  constexpr int LPR = P / 4, SB = strip_bytes(P);
   wait_for_stream();
   const int lane = threadIdx.x & 31, sub = lane % LPR, g = sub / 8, l = sub % 8;
-  const int64_t w = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  const int64_t w = int64_t(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
   const int chunks = (a.heads + kHeads - 1) / kHeads;
   const int64_t i = w / chunks;
   const int h0 = static_cast<int>(w - i * chunks) * kHeads;
   if (i >= a.n) return;
   const int slot = a.slots[i];
-  const int page = slot >= 0 ? slot / a.bs : 0, row = slot - page * a.bs, t = row % kStrip;
+  const int page = slot >= 0 ? div(slot, a.by_bs) : 0, row = slot - page * a.bs, t = row % kStrip;
   const bool in = slot >= 0 && page < a.n_pages;
   if (slot >= 0 && !in && lane == 0 && h0 == 0) report(a.status, RBA_ERR_BOUNDS, kWherePaged, slot);
   if (sub * 4 >= a.dim) return;
@@ -303,7 +357,16 @@ RowArgs row_args(const rba_paged* s, const int32_t* slots, int n) {
   a.bs = s->d.page_size;
   a.strips = s->strips;
   a.n_pages = s->d.n_pages;
+  // a CTA per slot and head while that is at most one wave; else fewer CTAs look through more slots
+  a.window = int64_t(n) * a.heads <= int64_t(num_sms()) * 16 ? 1 : 16;
+  a.by_bs = fast_div(a.bs);
+  a.by_heads = fast_div(a.heads);
   return a;
+}
+// CTAs of `slots` slots and one head each; 0 where a grid does not hold them.
+unsigned run_grid(const RowArgs& a, int slots) {
+  const int64_t grid = (int64_t(a.n) + slots - 1) / slots * a.heads;
+  return grid <= INT32_MAX ? static_cast<unsigned>(grid) : 0;
 }
 
 }  // namespace
@@ -329,17 +392,14 @@ extern "C" rba_status rba_paged_append(rba_paged* s, const int32_t* slots, int32
   const uintptr_t unit = 4 * dtype_size(s->d.dtype);
   a.vec = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % unit == 0 &&
           ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 3) == 0;
-  // a CTA per slot while that is at most one wave; else fewer CTAs look through more slots
-  a.window = int64_t(n) * a.heads <= int64_t(num_sms()) * 16 ? 1 : 16;
-  const int64_t grid = (int64_t(n) + a.window - 1) / a.window * a.heads;
-  const int64_t means = (int64_t(n) + 31) / 32 * ((a.heads + kRowWarps - 1) / kRowWarps);
-  if (grid > INT32_MAX || means > INT32_MAX) return RBA_ERR_UNSUPPORTED;
-#define RBA_APPEND(T_, P_)                                                                       \
-  do {                                                                                           \
-    RBA_CUDA_TRY(launch_dependent(append_kernel<T_, P_>, static_cast<unsigned>(grid),            \
-                                  append_warps<P_>() * 32, 0, stream, a));                       \
-    RBA_CUDA_TRY(launch_dependent(page_mean_kernel<P_>, static_cast<unsigned>(means), kRowThreads, \
-                                  0, stream, a));                                                \
+  const unsigned grid = run_grid(a, a.window);
+  if (grid == 0) return RBA_ERR_UNSUPPORTED;
+#define RBA_APPEND(T_, P_)                                                                      \
+  do {                                                                                          \
+    RBA_CUDA_TRY(launch_dependent(append_kernel<T_, P_>, grid, run_warps<P_>() * 32, 0, stream, \
+                                  a));                                                          \
+    RBA_CUDA_TRY(launch_dependent(page_mean_kernel<P_>, run_grid(a, 32), kMeanWarps * 32, 0,    \
+                                  stream, a));                                                  \
   } while (0)
   if (s->d.dtype == RBA_BF16) {
     if (s->pitch == 128) RBA_APPEND(__nv_bfloat16, 128);
@@ -363,13 +423,14 @@ extern "C" rba_status rba_paged_read(const rba_paged* s, const int32_t* slots, i
   RowArgs a = row_args(s, slots, n);
   a.k_out = k;
   a.v_out = v;
-  const int64_t blocks = (int64_t(n) * ((a.heads + 3) / 4) + kRowWarps - 1) / kRowWarps;
-  if (blocks > INT32_MAX) return RBA_ERR_UNSUPPORTED;
+  const int64_t grid =
+      (int64_t(n) * ((a.heads + kHeads - 1) / kHeads) + kReadWarps - 1) / kReadWarps;
+  if (grid > INT32_MAX) return RBA_ERR_UNSUPPORTED;
   const auto kernel = s->d.dtype == RBA_BF16
                           ? (s->pitch == 128 ? read_kernel<__nv_bfloat16, 128>
                                              : read_kernel<__nv_bfloat16, 64>)
                           : (s->pitch == 128 ? read_kernel<float, 128> : read_kernel<float, 64>);
   RBA_CUDA_TRY(
-      launch_dependent(kernel, static_cast<unsigned>(blocks), kRowThreads, 0, stream, a));
+      launch_dependent(kernel, static_cast<unsigned>(grid), kReadWarps * 32, 0, stream, a));
   return RBA_OK;
 }
