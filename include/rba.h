@@ -578,8 +578,8 @@ rba_status rba_paged_read(const rba_paged* store, const int32_t* slots, int32_t 
  *   idx  device int32 [n_requests][Hkv][k], written: pages of the request (columns of its table
  *        row) ascending; -1 past its candidates
  *   workspace >= rba_paged_select_workspace_size() (no contents are kept in it)
- * NaN scores are not supported.  Errors: INVALID_ARG, UNSUPPORTED (more than 16384 candidates
- * in max_pages), WORKSPACE, CUDA. */
+ * NaN scores are not supported.  Errors: INVALID_ARG, UNSUPPORTED (more
+ * than 16384 candidates in max_pages), WORKSPACE, CUDA. */
 rba_status rba_paged_select(const rba_paged* store, const void* q, int64_t q_request_stride,
                             int64_t q_head_stride, int32_t n_requests, int32_t k, int32_t sink,
                             int32_t window, int32_t* idx, void* workspace, size_t ws_bytes,

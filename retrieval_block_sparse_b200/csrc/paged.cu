@@ -7,7 +7,7 @@ namespace rba {
 namespace {
 
 constexpr int kTableThreads = 1024;
-constexpr int kPer = kMaxRequests / kTableThreads;  // requests a thread scans
+constexpr int kPer = kMaxRequests / kTableThreads;  // requests a thread scans at most
 
 struct TableArgs {
   const int32_t* by;      // extend: new tokens a request; truncate: tokens it keeps
@@ -19,14 +19,50 @@ struct TableArgs {
   int32_t* slots;
   int32_t* starts;
   int n_requests, bs, max_pages, n_pages, n_slots;
+  int per;                // requests a thread scans: ceil(n_requests / kTableThreads)
+  FastDiv by_bs;
 };
 
-__device__ __forceinline__ int pages_of(int tokens, int bs) { return (tokens + bs - 1) / bs; }
+__device__ __forceinline__ int pages_of(const TableArgs& a, int tokens) {
+  const int full = div(tokens, a.by_bs);
+  return full + (tokens > full * a.bs);
+}
+
+// Exclusive scans of two values a thread over the CTA; all[] receives the sums.
+__device__ __forceinline__ void block_scan_two(int64_t* v, int64_t (*s_w)[32], int64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t incl[2] = {v[0], v[1]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, incl[k], o);
+      if (lane >= o) incl[k] += t;
+    }
+  if (lane == 31) {
+    s_w[0][warp] = incl[0];
+    s_w[1][warp] = incl[1];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {  // (as many warps as lanes)
+    const int64_t mine = s_w[k][lane];
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += t;
+    }
+    all[k] = __shfl_sync(0xffffffffu, sum, 31);
+    v[k] = __shfl_sync(0xffffffffu, sum - mine, warp) + incl[k] - v[k];
+  }
+}
 
 // The last CTA of the call to arrive (thread 0 decides; every thread gets the answer).  The
 // arrival count is left zero.
 __device__ __forceinline__ bool last_cta(int32_t* count, int* s_last) {
   __syncthreads();
+  if (gridDim.x == 1) return true;
   if (threadIdx.x == 0) {
     __threadfence();
     const int n = atomicAdd(count, 1);
@@ -50,58 +86,57 @@ __device__ __forceinline__ bool last_cta(int32_t* count, int* s_last) {
 // (too few pages, a table row too short, a bad count) changes nothing.
 __global__ void __launch_bounds__(kTableThreads) extend_kernel(TableArgs a) {
   __shared__ int32_t s_start[kMaxRequests + 1], s_page[kMaxRequests + 1];
-  __shared__ int64_t s_w[32];
+  __shared__ int64_t s_w[2][32];
   __shared__ int s_last;
   wait_for_stream();
-  const int tid = threadIdx.x, R = a.n_requests;
-  int len[kPer], add[kPer];
-  int64_t tok = 0, pag = 0;
+  const int tid = threadIdx.x, R = a.n_requests, r0 = tid * a.per;
+  int len[kPer], add[kPer], need[kPer];
+  int64_t sum[2] = {0, 0}, all[2];  // tokens, pages
   int bad = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int r = tid * kPer + i;
     len[i] = add[i] = 0;
-    if (r < R) {
-      len[i] = a.lens[r];
-      add[i] = a.by[r];
-      const int64_t room = int64_t(a.max_pages) * a.bs;
-      if (len[i] < 0 || add[i] < 0 || int64_t(len[i]) + add[i] > room) {
-        bad = 1;
-        add[i] = 0;
-        len[i] = 0;
-      }
+    if (i < a.per && r0 + i < R) {
+      len[i] = a.lens[r0 + i];
+      add[i] = a.by[r0 + i];
     }
-    tok += add[i];
-    pag += pages_of(len[i] + add[i], a.bs) - pages_of(len[i], a.bs);
+  }
+  const int n_free = *a.n_free;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t room = int64_t(a.max_pages) * a.bs;
+    if (len[i] < 0 || add[i] < 0 || int64_t(len[i]) + add[i] > room) {
+      bad = 1;
+      len[i] = add[i] = 0;
+    }
+    need[i] = pages_of(a, len[i] + add[i]) - pages_of(a, len[i]);
+    sum[0] += add[i];
+    sum[1] += need[i];
   }
   bad = __syncthreads_or(bad);
-  const int n_free = *a.n_free;
-  int64_t tok_all, pag_all;
-  int64_t tok0 = block_scan64(tok, s_w, &tok_all);
-  int64_t pag0 = block_scan64(pag, s_w, &pag_all);
-  bad |= tok_all > a.n_slots || pag_all > n_free || n_free > a.n_pages;
+  block_scan_two(sum, s_w, all);
+  bad |= all[0] > a.n_slots || all[1] > n_free || n_free > a.n_pages;
   if (!bad) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int r = tid * kPer + i;
-      if (r < R) {
-        s_start[r] = static_cast<int>(tok0);
-        s_page[r] = static_cast<int>(pag0);
+      if (i < a.per && r0 + i < R) {
+        s_start[r0 + i] = static_cast<int>(sum[0]);
+        s_page[r0 + i] = static_cast<int>(sum[1]);
       }
-      tok0 += add[i];
-      pag0 += pages_of(len[i] + add[i], a.bs) - pages_of(len[i], a.bs);
+      sum[0] += add[i];
+      sum[1] += need[i];
     }
-    if (tid == 0) s_start[R] = static_cast<int>(tok_all);
+    if (tid == 0) s_start[R] = static_cast<int>(all[0]);
   }
   __syncthreads();
-  const int total = bad ? 0 : static_cast<int>(tok_all);
+  const int total = bad ? 0 : static_cast<int>(all[0]);
   const int step = gridDim.x * kTableThreads;
   for (int i = blockIdx.x * kTableThreads + tid; i < a.n_slots; i += step) {
     int slot = -1;
     if (i < total) {
       const int r = last_at_most(s_start, R, i);
-      const int len_r = a.lens[r], held = pages_of(len_r, a.bs);
-      const int pos = len_r + i - s_start[r], j = pos / a.bs, row = pos - j * a.bs;
+      const int len_r = a.lens[r], held = pages_of(a, len_r);
+      const int pos = len_r + i - s_start[r], j = div(pos, a.by_bs), row = pos - j * a.bs;
       int page;
       if (j < held) {
         page = a.table[int64_t(r) * a.max_pages + j];
@@ -122,54 +157,55 @@ __global__ void __launch_bounds__(kTableThreads) extend_kernel(TableArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (tid * kPer + i < R) a.lens[tid * kPer + i] = len[i] + add[i];
-  if (tid == 0) *a.n_free = n_free - static_cast<int>(pag_all);
+    if (i < a.per && r0 + i < R && add[i] != 0) a.lens[r0 + i] = len[i] + add[i];
+  if (tid == 0) *a.n_free = n_free - static_cast<int>(all[1]);
 }
 
 // Requests cut back to min(len_r, keep_r) tokens.  The pages past them go back to the free
 // list in the order opposite to extend's, so that a cut undoes the extension before it.
 __global__ void __launch_bounds__(kTableThreads) truncate_kernel(TableArgs a) {
   __shared__ int32_t s_page[kMaxRequests + 1];
-  __shared__ int64_t s_w[32];
+  __shared__ int64_t s_w[2][32];
   __shared__ int s_last;
   wait_for_stream();
-  const int tid = threadIdx.x, R = a.n_requests;
-  int kept[kPer], freed[kPer];
-  int64_t pag = 0;
+  const int tid = threadIdx.x, R = a.n_requests, r0 = tid * a.per;
+  int len[kPer], keep[kPer], kept[kPer], freed[kPer];
+  int64_t sum[2] = {0, 0}, all[2];  // (the first unused), pages
   int bad = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int r = tid * kPer + i;
-    kept[i] = freed[i] = 0;
-    if (r < R) {
-      const int len = a.lens[r], keep = a.by[r];
-      if (len < 0 || keep < 0 || len > int64_t(a.max_pages) * a.bs) {
-        bad = 1;
-      } else {
-        kept[i] = min(len, keep);
-        freed[i] = pages_of(len, a.bs) - pages_of(kept[i], a.bs);
-      }
+    len[i] = keep[i] = 0;
+    if (i < a.per && r0 + i < R) {
+      len[i] = a.lens[r0 + i];
+      keep[i] = a.by[r0 + i];
     }
-    pag += freed[i];
+  }
+  const int n_free = *a.n_free;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (len[i] < 0 || keep[i] < 0 || len[i] > int64_t(a.max_pages) * a.bs) {
+      bad = 1;
+      len[i] = keep[i] = 0;
+    }
+    kept[i] = min(len[i], keep[i]);
+    freed[i] = pages_of(a, len[i]) - pages_of(a, kept[i]);
+    sum[1] += freed[i];
   }
   bad = __syncthreads_or(bad);
-  const int n_free = *a.n_free;
-  int64_t pag_all;
-  int64_t pag0 = block_scan64(pag, s_w, &pag_all);
-  bad |= n_free < 0 || n_free + pag_all > a.n_pages;
+  block_scan_two(sum, s_w, all);
+  bad |= n_free < 0 || n_free + all[1] > a.n_pages;
   if (!bad) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int r = tid * kPer + i;
-      if (r < R) s_page[r] = static_cast<int>(pag0);
-      pag0 += freed[i];
+      if (i < a.per && r0 + i < R) s_page[r0 + i] = static_cast<int>(sum[1]);
+      sum[1] += freed[i];
     }
   }
   __syncthreads();
-  const int total = bad ? 0 : static_cast<int>(pag_all);
+  const int total = bad ? 0 : static_cast<int>(all[1]);
   for (int i = blockIdx.x * kTableThreads + tid; i < total; i += gridDim.x * kTableThreads) {
     const int r = last_at_most(s_page, R, i);
-    const int j = pages_of(min(a.lens[r], a.by[r]), a.bs) + i - s_page[r];
+    const int j = pages_of(a, min(a.lens[r], a.by[r])) + i - s_page[r];
     a.free_pages[n_free + total - 1 - i] = a.table[int64_t(r) * a.max_pages + j];
   }
   if (!last_cta(a.status + 4, &s_last)) return;
@@ -179,7 +215,7 @@ __global__ void __launch_bounds__(kTableThreads) truncate_kernel(TableArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
-    if (tid * kPer + i < R) a.lens[tid * kPer + i] = kept[i];
+    if (i < a.per && r0 + i < R) a.lens[r0 + i] = kept[i];
   if (tid == 0) *a.n_free = n_free + total;
 }
 
@@ -195,6 +231,8 @@ TableArgs table_args(const rba_paged* s, const int32_t* by, int n_requests) {
   a.bs = s->d.page_size;
   a.max_pages = s->d.max_pages;
   a.n_pages = s->d.n_pages;
+  a.per = (n_requests + kTableThreads - 1) / kTableThreads;
+  a.by_bs = fast_div(a.bs);
   return a;
 }
 

@@ -37,8 +37,8 @@
 
 #include <algorithm>
 
-#include "decode_persist.cuh"
 #include "paged.cuh"
+#include "paged_ring.cuh"
 
 namespace rba {
 namespace {
@@ -105,28 +105,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-// Whether the barrier's phase is over, for the whole warp (shared-memory address).
-__device__ __forceinline__ bool phase_over(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " vote.sync.all.pred p, p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-// Arms the barrier with `bytes` where `arm`, and copies `bytes1` to dst where they are not 0
-// (predicated: no branch).
-__device__ __forceinline__ void arm_and_copy(uint32_t bar, int arm, uint32_t bytes, uint32_t dst,
-                                             const void* src, uint32_t bytes1) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 p, %0, 0;\n setp.ne.u32 q, %4, 0;\n"
-      " @p mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%1], %2;\n"
-      " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%3], [%5], %4, [%1];\n"
-      "}\n" ::"r"(arm), "r"(bar), "r"(bytes), "r"(dst), "r"(bytes1), "l"(src)
-      : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -742,21 +720,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
 #pragma unroll 1
     for (; j < till; ++j) {
       const uint32_t bar = bar0 + (j & 1) * 8, parity = (j >> 1) & 1;
-      if (!phase_over(bar, parity)) {
-        const unsigned long long t0 = now_ns();
-        bool over, late;
-        do {
-          over = phase_over(bar, parity);
-          late = __shfl_sync(0xffffffffu, now_ns() - t0 > kTimeoutNs, 0);
-        } while (!over && !late);
-        if (!over) {
-          if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, j);
-          // copies in flight land before the warp goes on without its pairs
-          mbar_drain(bars + (j & 1), parity);
-          if (j + 1 < mine) mbar_drain(bars + (~j & 1), ((j + 1) >> 1) & 1);
-          mine = till = 0;
-          break;
-        }
+      if (!await_phase(bar, parity)) {
+        if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, j);
+        // copies in flight land before the warp goes on without its pairs
+        mbar_drain(bars + (j & 1), parity);
+        if (j + 1 < mine) mbar_drain(bars + (~j & 1), ((j + 1) >> 1) & 1);
+        mine = till = 0;
+        break;
       }
       // (pair j + 1 was issued last: in j's round or the next)
       const int r2 = __shfl_sync(0xffffffffu, (j & 15) == 15 && j + 1 < mine ? rows_before : rows,

@@ -1,17 +1,20 @@
 // Paged 4-bit memory: selection of each request's best pages.
 //
-// score(r, h, j) = sum over dims of (sum over the group's q heads of q) * rep[table[r][j]][h],
-// accumulated in 64 bits and rounded once to 32, for request r's candidate pages j; the k best
-// per (request, kv head), ties to the lower page.  A 32-bit accumulation would leave the order
-// of near pages to the order of the sum.
+// score(r, h, j) = sum over dims of (sum over the group's q heads of q) * rep[table[r][j]][h] for
+// request r's candidate pages j, rounded once to 32 bits; the k best per (request, kv head), ties to
+// the lower page.  A 32-bit accumulation would leave the order of near pages to the order of the
+// sum, so it is held in 64.  (In two 32-bit words, with exact products and sums, the same bits cost
+// a fifth more time at 86 MB of page means: five times the instructions.)
 #include "paged.cuh"
+#include "paged_ring.cuh"
 
 namespace rba {
 namespace {
 
 constexpr int kScoreThreads = 256;
 constexpr int kScoreCtas = 2;  // per SM
-constexpr int kBatch = 8;      // candidate rows in flight per lane
+constexpr int kBatch = 8;      // candidate rows that a lane has a share of at a time
+constexpr int kRingPlaces = 3; // batches in a warp's ring: 4 KB each
 
 struct SelectArgs {
   const void* q;
@@ -22,6 +25,7 @@ struct SelectArgs {
   int32_t* status;
   float* scores;  // [R][Hkv][row]
   int R, heads, group, dim, bs, max_pages, n_pages, sink, window, row;
+  bool q_vec;  // rows of q start on a boundary of four elements
 };
 
 // pre[r] = batches of `per` candidates of the requests before r (one kv head); returns their sum.
@@ -46,18 +50,27 @@ __device__ int64_t scan_batches(const SelectArgs& a, int per, int32_t* pre, int3
   return run;
 }
 
-// A warp takes a run of batches of PER candidates: the page numbers of the next batch are loaded
-// while this one's rows are; the rows' sums are added over lanes by halving exchanges (each step
-// halves the rows a lane carries), two or three of a double per row instead of five.
+// A warp takes a run of batches of PER candidates, through its own ring of bulk copies (a row is one
+// run of bytes): 4 KB a batch, three batches on their way, whatever the warp is computing.  (Loaded
+// into registers a batch ahead, the rows of 16 warps an SM left its memory idle half the time: 26 us
+// for 86 MB.)  The page numbers of the batch to be copied next are loaded one copy ahead.  The sums
+// are added over lanes by halving exchanges (each step halves the rows a lane carries): two or three
+// per row instead of five.
 template <typename T, int P>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(SelectArgs a) {
   constexpr int LPR = P / 4, RPW = 32 / LPR;  // lanes a row, rows a warp reads at once
-  constexpr int PER = kBatch * RPW;
-  extern __shared__ int32_t sm[];
-  __shared__ int64_t s_w[kScoreThreads / 32];
+  constexpr int PER = kBatch * RPW, ROW = P * 4, PLACE = PER * ROW;
+  constexpr int kScoreWarps = kScoreThreads / 32;
+  extern __shared__ __align__(128) char sm[];
+  __shared__ int64_t s_w[kScoreWarps];
+  __shared__ uint64_t s_bars[kScoreWarps][kRingPlaces];
+  int32_t* pre = reinterpret_cast<int32_t*>(sm + kScoreWarps * kRingPlaces * PLACE);
+  int32_t* ncand = pre + a.R;
+  uint64_t* bars = s_bars[threadIdx.x >> 5];
+  if ((threadIdx.x & 31) < kRingPlaces) mbar_init(bars + (threadIdx.x & 31), 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   wait_for_stream();
-  int32_t* pre = sm;
-  int32_t* ncand = sm + a.R;
   const int64_t one = scan_batches(a, PER, pre, ncand, s_w);
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const int first = a.sink / a.bs;
@@ -67,84 +80,117 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
   const int64_t w = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
   const int64_t b0 = all * w / nw, b1 = all * (w + 1) / nw;
   if (b0 >= b1) return;
-  int r = last_at_most(pre, a.R, static_cast<int32_t>(b0 / a.heads));
-  int nc = ncand[r], nb = (nc + PER - 1) / PER;
-  int h, c0;
+  struct Pos {
+    int r, h, c0, nc;  // request, kv head, first candidate of the batch, the request's candidates
+  } at;
+  at.r = last_at_most(pre, a.R, static_cast<int32_t>(b0 / a.heads));
+  at.nc = ncand[at.r];
   {
-    const int64_t in = b0 - int64_t(pre[r]) * a.heads;
-    h = static_cast<int>(in / nb);
-    c0 = static_cast<int>(in - int64_t(h) * nb) * PER;
+    const int nb = (at.nc + PER - 1) / PER;
+    const int64_t in = b0 - int64_t(pre[at.r]) * a.heads;
+    at.h = static_cast<int>(in / nb);
+    at.c0 = static_cast<int>(in - int64_t(at.h) * nb) * PER;
   }
-  const auto page_of = [&](int r_, int c0_, int nc_) {  // lane i: page of candidate c0 + i, or -1
-    if (lane >= PER || c0_ + lane >= nc_) return -1;
-    const int page = a.table[int64_t(r_) * a.max_pages + first + c0_ + lane];
+  const auto advance = [&](Pos p) {  // (called where a batch is left, so a request with candidates is)
+    p.c0 += PER;
+    if (p.c0 < p.nc) return p;
+    p.c0 = 0;
+    if (++p.h < a.heads) return p;
+    p.h = 0;
+    do ++p.r;
+    while (ncand[p.r] == 0);
+    p.nc = ncand[p.r];
+    return p;
+  };
+  const auto page_of = [&](const Pos& p) {  // lane i: page of candidate c0 + i, or -1
+    if (lane >= PER || p.c0 + lane >= p.nc) return -1;
+    const int page = a.table[int64_t(p.r) * a.max_pages + first + p.c0 + lane];
     if (page >= 0 && page < a.n_pages) return page;
     report(a.status, RBA_ERR_BOUNDS, kWherePaged, page);
     return -1;
   };
-  int page = page_of(r, c0, nc);
-  bool fresh = true;
-  double q[4] = {0, 0, 0, 0};
-  for (int64_t b = b0; b < b1; ++b) {
-    float4 x[kBatch];
+  double q[4];
+  const auto load_q = [&](const Pos& p) {  // the group's sum
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int p = __shfl_sync(0xffffffffu, page, u * RPW + sub);
-      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p >= 0)
-        x[u] = __ldg(reinterpret_cast<const float4*>(a.rep + (int64_t(p) * a.heads + h) * P) + l);
-    }
-    if (fresh) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = 0;
-      if (l * 4 < a.dim) {
-        const T* src = static_cast<const T*>(a.q) + r * a.q_req + int64_t(h) * a.group * a.q_head;
+    for (int e = 0; e < 4; ++e) q[e] = 0;
+    if (l * 4 >= a.dim) return;
+    const T* src = static_cast<const T*>(a.q) + p.r * a.q_req + int64_t(p.h) * a.group * a.q_head;
 #pragma unroll 4
-        for (int i = 0; i < a.group; ++i)
+    for (int i = 0; i < a.group; ++i) {
+      float f[4];
+      load4(src + i * a.q_head + l * 4, a.q_vec, f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            q[e] += static_cast<double>(Elem<T>::to_f32(src[i * a.q_head + l * 4 + e]));
-      }
+      for (int e = 0; e < 4; ++e) q[e] += static_cast<double>(f[e]);
     }
-    // the batch after this one
-    const int64_t unit = int64_t(r) * a.heads + h;
-    const int at = c0, most = nc;
-    if (b + 1 < b1) {
-      c0 += PER;
-      fresh = c0 >= nc;
-      if (fresh) {
-        c0 = 0;
-        if (++h == a.heads) {
-          h = 0;
-          do ++r;
-          while (ncand[r] == 0);  // (a batch is left, so a request with candidates is)
-          nc = ncand[r];
-        }
-      }
-      page = page_of(r, c0, nc);
+  };
+  const char* ring = sm + (threadIdx.x >> 5) * kRingPlaces * PLACE;
+  const uint32_t ring0 = smem_u32(ring) + lane * ROW, bar0 = smem_u32(bars);
+  // copies run ahead of the sums: `ahead` is the next batch to copy, `page` its pages
+  Pos ahead = at;
+  int page = page_of(at);
+  unsigned rows[kRingPlaces];  // lanes whose candidate's row is in the place
+  const auto issue = [&](int n) {  // the warp's n-th batch (b0 + n) into place n % kRingPlaces
+    if (b0 + n >= b1) return;
+    const int i = n % kRingPlaces;
+    const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
+#pragma unroll
+    for (int j = 0; j < kRingPlaces; ++j)
+      if (j == i) rows[j] = there;
+    arm_and_copy(bar0 + i * 8, lane == 0, ROW * __popc(there), ring0 + i * PLACE,
+                 a.rep + (int64_t(page) * a.heads + ahead.h) * P, page >= 0 ? ROW : 0);
+    if (b0 + n + 1 < b1) {
+      ahead = advance(ahead);
+      page = page_of(ahead);
     }
+  };
+#pragma unroll
+  for (int n = 0; n < kRingPlaces; ++n) issue(n);
+  load_q(at);
+  const int batches = static_cast<int>(b1 - b0);
+  for (int n = 0; n < batches; ++n) {
+    const int i = n % kRingPlaces;
+    if (!await_phase(bar0 + i * 8, (n / kRingPlaces) & 1)) {
+      if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, n);
+      for (int m = n; m < n + kRingPlaces && m < batches; ++m)  // copies in flight land first
+        mbar_drain(bars + m % kRingPlaces, (m / kRingPlaces) & 1);
+      return;
+    }
+    unsigned there = 0;
+#pragma unroll
+    for (int j = 0; j < kRingPlaces; ++j)
+      if (j == i) there = rows[j];
     double s[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      s[u] = q[0] * x[u].x;
-      s[u] = fma(q[1], double(x[u].y), s[u]);
-      s[u] = fma(q[2], double(x[u].z), s[u]);
-      s[u] = fma(q[3], double(x[u].w), s[u]);
+      const float4 x = *reinterpret_cast<const float4*>(ring + i * PLACE + (u * RPW + sub) * ROW + l * 16);
+      s[u] = q[0] * x.x;
+      s[u] = fma(q[1], double(x.y), s[u]);
+      s[u] = fma(q[2], double(x.z), s[u]);
+      s[u] = fma(q[3], double(x.w), s[u]);
+    }
+    const Pos done = at;
+    __syncwarp();
+    issue(n + kRingPlaces);
+    if (n + 1 < batches) {
+      at = advance(at);
+      if (at.c0 == 0) load_q(at);
     }
     // after the steps of width 4, 2, 1 a lane carries row bits (l & 4, l & 2, l & 1) of the eight
 #pragma unroll
-    for (int n = kBatch / 2; n > 0; n >>= 1) {
-      const bool up = (l & n) != 0;
+    for (int w = kBatch / 2; w > 0; w >>= 1) {
+      const bool up = (l & w) != 0;
 #pragma unroll
-      for (int u = 0; u < n; ++u) {
-        const double give = up ? s[u] : s[u + n], keep = up ? s[u + n] : s[u];
-        s[u] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+      for (int u = 0; u < w; ++u) {
+        const double give = up ? s[u] : s[u + w], keep = up ? s[u + w] : s[u];
+        s[u] = keep + __shfl_xor_sync(0xffffffffu, give, w);
       }
     }
 #pragma unroll
     for (int o = kBatch; o < LPR; o <<= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
-    const int c = at + (l % kBatch) * RPW + sub;
-    if (l < kBatch && c < most) a.scores[unit * a.row + c] = static_cast<float>(s[0]);
+    const int r = (l % kBatch) * RPW + sub, c = done.c0 + r;
+    if (l < kBatch && c < done.nc)  // (a page that is not in the pool scores 0)
+      a.scores[(int64_t(done.r) * a.heads + done.h) * a.row + c] =
+          (there >> r) & 1u ? static_cast<float>(s[0]) : 0.f;
   }
 }
 
@@ -196,13 +242,17 @@ extern "C" rba_status rba_paged_select(const rba_paged* s, const void* q,
   a.sink = sink;
   a.window = window;
   a.row = row;
+  a.q_vec = reinterpret_cast<uintptr_t>(q) % (4 * dtype_size(s->d.dtype)) == 0 &&
+            ((q_request_stride | q_head_stride) & 3) == 0;
   if (row > 0) {
-    const size_t smem = size_t(n_requests) * 8;
+    const size_t smem = size_t(kScoreThreads / 32) * kRingPlaces * kBatch * 512 +
+                        size_t(n_requests) * 8;
     const auto kernel =
         s->d.dtype == RBA_BF16
             ? (s->pitch == 128 ? paged_score_kernel<__nv_bfloat16, 128>
                                : paged_score_kernel<__nv_bfloat16, 64>)
             : (s->pitch == 128 ? paged_score_kernel<float, 128> : paged_score_kernel<float, 64>);
+    RBA_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kernel), smem));
     RBA_CUDA_TRY(launch_dependent(kernel, static_cast<unsigned>(num_sms() * kScoreCtas),
                                   kScoreThreads, smem, stream, a));
   }
