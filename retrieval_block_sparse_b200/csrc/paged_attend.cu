@@ -13,9 +13,9 @@
 // takes the scale, w = p s_tg 2^e, split the same way.  Softmax statistics, both products'
 // accumulators and the merges are 32-bit.
 //
-// Layout.  One warp takes a pair of strips of 16 tokens at a time.  K codes are the A operand of the first product
-// (16 tokens x 16 dims), q its B; V codes, read in token pairs, are the A operand of the second
-// (16 dims x 16 tokens), and the weights its B after 8 x 8 transposes in registers.  Up to four
+// Layout.  One warp takes a pair of strips of 16 tokens at a time.  K codes are the A operand of
+// the first product (16 tokens x 16 dims), q its B; V codes, read in token pairs, are the A operand
+// of the second (16 dims x 16 tokens), and the weights its B after 8 x 8 transposes in registers.  Up to four
 // q heads to a kv head fill the eight columns with their hi and lo halves ("packed": one product
 // for both); five to eight take a column each and a second product for the lo halves ("wide":
 // the accumulators stay 32 registers); larger groups are cut into chunks of eight.
@@ -53,6 +53,7 @@ constexpr int kTeamCost = 10, kAloneCost = 3;
 constexpr int kTeamLeast = kWarps, kAloneLeast = 2;
 // Warps work alone where the longest unit is then cut into at most this many parts.
 constexpr int kAloneParts = 24;
+constexpr int kFold = 16;  // pairs that a warp sums in the matrix unit's accumulators
 // Units are taken whole where none can be longer than this: by single warps, or by CTAs where those
 // suffice for one unit each.
 constexpr int kWholePairs = 8;
@@ -225,9 +226,10 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // (a 
 // Parts of the q operand (in shared memory, read group by group): hi, and for wide 32-bit q lo.
 template <bool kWide, bool kLo> constexpr int q_parts() { return kWide && kLo ? 2 : 1; }
 
-// A warp's running state for the unit's heads (y: logits over fac >= 0, in log2 units); lane (t, c) = (lane / 4, lane % 4) holds head c
-// (packed) or heads 2 c and 2 c + 1 (wide).  A weight is 2^(y - m), y the logit in log2 units;
-// the values' scales are taken times 2^e, which keeps weight x scale within a half's range.
+// A warp's running state for the unit's heads; lane (t, c) = (lane / 4, lane % 4) holds head c
+// (packed) or heads 2 c and 2 c + 1 (wide).  A weight is 2^(y fac - m), y fac the logit in log2
+// units, fac >= 0; the values' scales are taken times 2^e, which keeps weight x scale within a
+// half's range.
 template <int P, bool kWide> struct State {
   static constexpr int HL = kWide ? 2 : 1, G = P / 32;
   float m[HL], l[HL];    // reference; this lane's part of the weights' sum
@@ -396,8 +398,8 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid2,
 }
 
 // Shared memory: rings | warp states (warps working alone: their q operands) | q operand |
-// factors | barriers | pairs and units before each request.  (With up to 590 requests two CTAs fit an
-// SM in every form.)
+// factors | barriers | pairs and units before each request.  (With up to 590 requests two CTAs fit
+// an SM in every form.)
 template <int P, bool kWide, bool kLo> struct Smem {
   static constexpr int H = kWide ? 8 : 4;
   static constexpr int kRow = P + 4;            // out, then m and l
@@ -438,7 +440,8 @@ __device__ __forceinline__ void stage_q(const PagedAttendArgs& a, const float* x
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float v = x[e] * up0 * up1, hi = __half2float(__float2half_rn(v)), lo = v - hi;
-    const float hi_n = __shfl_xor_sync(0xffffffffu, hi, 1), lo_n = __shfl_xor_sync(0xffffffffu, lo, 1);
+    const float hi_n = __shfl_xor_sync(0xffffffffu, hi, 1);
+    const float lo_n = __shfl_xor_sync(0xffffffffu, lo, 1);
     if (lane * 4 >= P) continue;
     // even lanes hold the first dim of a pair and write its hi part, odd lanes the lo part
     const uint32_t word = odd ? pack_half2(lo_n, lo) : pack_half2(hi, hi_n);
@@ -505,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   for (int base = 0; base < a.R; base += kThreads) {
     const int r = base + tid;
     int n = 0;
-    if (r < a.R) n = (unit_map(a, paged_len(a.lens, r, a.bs, a.max_pages, a.status)).total() + 1) / 2;
+    if (r < a.R)
+      n = (unit_map(a, paged_len(a.lens, r, a.bs, a.max_pages, a.status)).total() + 1) / 2;
     int64_t tot;
     const int64_t ex =  // (two barriers: s_long is set by now)
         run + block_scan64(int64_t(n) << 16 | int64_t(n > 0), s_w, &tot);
@@ -516,7 +520,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     if (n > 0) atomicMax(&s_long, n);
     run += tot;
   }
-  const uint32_t pairs = static_cast<uint32_t>(run >> 16), some = static_cast<uint32_t>(run & 0xffff);
+  const uint32_t pairs = static_cast<uint32_t>(run >> 16);
+  const uint32_t some = static_cast<uint32_t>(run & 0xffff);
   if (tid == 0) {
     pre[a.R] = static_cast<int32_t>(pairs);
     cnt[a.R] = static_cast<uint16_t>(some);
@@ -702,70 +707,112 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     }
     const uint32_t* qw = q_place(at_place);
     float fac[HL];
-    State<P, kWide> st;
-    st.e = kMostE;
-    st.most = pow2(kScaleTop - kMostE);
 #pragma unroll
-    for (int i = 0; i < HL; ++i) {
-      fac[i] = fac_place(at_place)[HL * (lane & 3) + i];
-      st.m[i] = st.top[i] = -INFINITY;
-      st.l[i] = 0.f;
-    }
-#pragma unroll
-    for (int b = 0; b < 2 * G; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) st.acc[b][i] = 0.f;
-
-    int till = min(mine, pairs_below(stop));
-#pragma unroll 1
-    for (; j < till; ++j) {
-      const uint32_t bar = bar0 + (j & 1) * 8, parity = (j >> 1) & 1;
-      if (!await_phase(bar, parity)) {
-        if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, j);
-        // copies in flight land before the warp goes on without its pairs
-        mbar_drain(bars + (j & 1), parity);
-        if (j + 1 < mine) mbar_drain(bars + (~j & 1), ((j + 1) >> 1) & 1);
-        mine = till = 0;
-        break;
-      }
-      // (pair j + 1 was issued last: in j's round or the next)
-      const int r2 = __shfl_sync(0xffffffffu, (j & 15) == 15 && j + 1 < mine ? rows_before : rows,
-                                 2 * (j & 15));
-      if (r2 != 0)
-        pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + (j & 1) * 2 * SB), r2, qw,
-                                 fac, st);
-      __syncwarp();
-      issue(j + kStages);
-    }
-
-    // the warp's state, in its lanes: dims 32 g + 4 t + {0..3} of heads HL c ..
+    for (int i = 0; i < HL; ++i) fac[i] = fac_place(at_place)[HL * (lane & 3) + i];
+    // Every kFold pairs the state is added to its place in memory and starts anew: the matrix unit
+    // cuts its sums towards zero, which over a long line would add up.
+    const auto part_of = [&] { return a.parts + (int64_t(worker) * 2 + later) * S::kSlot; };
     const int t = lane >> 2, c = lane & 3;
-    float4 o[HL][G];
-    {
-      const float down = pow2(-st.e);
+    State<P, kWide> st;
+    float4 o[HL][G];  // the warp's state in its lanes: dims 32 g + 4 t + {0..3} of heads HL c ..
+    int till = min(mine, pairs_below(stop));
+    bool held = false;
+#pragma unroll 1
+    while (true) {
+      st.e = kMostE;
+      st.most = pow2(kScaleTop - kMostE);
 #pragma unroll
       for (int i = 0; i < HL; ++i) {
+        st.m[i] = st.top[i] = -INFINITY;
+        st.l[i] = 0.f;
+      }
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
+      for (int b = 0; b < 2 * G; ++b)
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          float y[4];
+        for (int i = 0; i < 4; ++i) st.acc[b][i] = 0.f;
+
+      const int pause = min(till, j + kFold);
+#pragma unroll 1
+      for (; j < pause; ++j) {
+        const uint32_t bar = bar0 + (j & 1) * 8, parity = (j >> 1) & 1;
+        if (!await_phase(bar, parity)) {
+          if (lane == 0) report(a.status, RBA_ERR_TIMEOUT, kWherePaged, j);
+          // copies in flight land before the warp goes on without its pairs
+          mbar_drain(bars + (j & 1), parity);
+          if (j + 1 < mine) mbar_drain(bars + (~j & 1), ((j + 1) >> 1) & 1);
+          mine = till = 0;
+          break;
+        }
+        // (pair j + 1 was issued last: in j's round or the next)
+        const int r2 = __shfl_sync(0xffffffffu, (j & 15) == 15 && j + 1 < mine ? rows_before : rows,
+                                   2 * (j & 15));
+        if (r2 != 0)
+          pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + (j & 1) * 2 * SB), r2,
+                                   qw, fac, st);
+        __syncwarp();
+        issue(j + kStages);
+      }
+
+      {
+        const float down = pow2(-st.e);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float* d = st.acc[2 * g + x / 2];
-            y[x] = (kWide ? d[2 * (x % 2) + i] : d[2 * (x % 2)] + d[2 * (x % 2) + 1]) * 0x1p9f * down;
+        for (int i = 0; i < HL; ++i) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            float y[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float* d = st.acc[2 * g + x / 2];
+              y[x] = (kWide ? d[2 * (x % 2) + i] : d[2 * (x % 2)] + d[2 * (x % 2) + 1]) * 0x1p9f *
+                     down;
+            }
+            // (the odd rows hold the even dim plus 16 times theirs)
+            o[i][g] = make_float4(y[0], (y[1] - y[0]) * 0.0625f, y[2], (y[3] - y[2]) * 0.0625f);
           }
-          // (the odd rows hold the even dim plus 16 times theirs)
-          o[i][g] = make_float4(y[0], (y[1] - y[0]) * 0.0625f, y[2], (y[3] - y[2]) * 0.0625f);
         }
       }
+      float* to = alone ? part_of() : slots + warp * S::kSlot;
+      if (held) {  // with what was put there before
+#pragma unroll
+        for (int i = 0; i < HL; ++i) {
+          const float* s = to + (HL * c + i) * S::kRow;
+          const float pm = s[P], pl = s[P + 1], m = fmaxf(st.m[i], pm);
+          const float f0 = st.m[i] == m ? 1.f : ex2(st.m[i] - m), f1 = pm == m ? 1.f : ex2(pm - m);
+          st.m[i] = m;
+          st.l[i] = st.l[i] * f0 + pl * f1;
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float4 x = *reinterpret_cast<const float4*>(s + 32 * g + 4 * t);
+            o[i][g] = make_float4(o[i][g].x * f0 + x.x * f1, o[i][g].y * f0 + x.y * f1,
+                                  o[i][g].z * f0 + x.z * f1, o[i][g].w * f0 + x.w * f1);
+          }
+        }
+      }
+      if (j >= till) break;
+      __syncwarp();  // (read by every lane of a head, written by one)
+#pragma unroll
+      for (int i = 0; i < HL; ++i) {
+        float* s = to + (HL * c + i) * S::kRow;
+#pragma unroll
+        for (int g = 0; g < G; ++g) *reinterpret_cast<float4*>(s + 32 * g + 4 * t) = o[i][g];
+        if (t == 0) {
+          s[P] = st.m[i];
+          s[P + 1] = st.l[i];
+        }
+      }
+      __syncwarp();
+      held = true;
     }
+
     const bool more = stop < end;
     const At p = place(at);  // (again: nothing of it is kept over the loop)
     const bool whole = at == p.u0 && stop == p.u0 + p.n;
     const int64_t row0 = (int64_t(p.r) * a.heads + p.h) * a.group + p.h0;
-    float* part = a.parts + (int64_t(worker) * 2 + later) * S::kSlot;
+    float* part = part_of();
     float* to = alone ? part : slots + warp * S::kSlot;
+    if (held) __syncwarp();  // (as above)
     if (at == p.u0 && lane == 0 && (alone || warp == 0)) {
       // this worker holds the unit's first pair; the last one's holds its last
       const uint32_t x0 = cost_at(p);
