@@ -1009,7 +1009,9 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
   // share two pages)
   const int64_t unit = ((int64_t(s->d.max_pages) + 2) * s->strips + 1) / 2 + kTeamCost;
   const int64_t units = int64_t(n_requests) * s->d.n_kv_heads * chunks_of(s);
-  if (unit > INT32_MAX || unit * units > INT32_MAX) return RBA_ERR_UNSUPPORTED;
+  if (unit > INT32_MAX || unit * units > INT32_MAX ||
+      int64_t(n_requests) * s->d.n_q_heads > INT32_MAX)
+    return RBA_ERR_UNSUPPORTED;
   PagedAttendArgs a = {};
   a.q = q;
   a.q_req = q_request_stride;

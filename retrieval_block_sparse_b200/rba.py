@@ -505,6 +505,8 @@ class PagedStore:
     def __init__(self, *, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_requests,
                  max_pages, dtype="bf16", device="cuda", pool=None, rep=None, table=None,
                  lens=None, free=None, n_free=None):
+        if dtype not in ("bf16", "f32", torch.bfloat16, torch.float32):
+            raise ValueError(f"dtype: expected bf16 or f32, got {dtype}")
         self.dtype = BF16 if dtype in ("bf16", torch.bfloat16) else F32
         self.Hq, self.Hkv, self.D, self.page_size = n_q_heads, n_kv_heads, head_dim, page_size
         self.n_pages, self.max_requests, self.max_pages = n_pages, max_requests, max_pages
@@ -684,6 +686,21 @@ class PagedStore:
         self._call("rba_paged_attend", qp, qr, qh, R, ip, k, sink, window, scale, op, lp,
                    *self._bytes(workspace))
         return out, lse
+
+    # -- whole decode step -----------------------------------------------------------
+    def decode_step(self, q, k_new, v_new, n_new, k, sink, window, *, scale=None, slots=None,
+                    starts=None, idx=None, out=None, lse=None, select_workspace=None,
+                    workspace=None):
+        """One step of every request: request r grows by n_new[r] tokens, whose rows are packed in
+        k_new, v_new [n][Hkv][D] (n may be larger: rows past them are ignored), then q [R][Hq][D]
+        attends to sink, its k best pages and window.  Returns (idx, out, lse).  With every
+        buffer given it can be captured once and replayed."""
+        slots, _ = self.extend(n_new, k_new.shape[0], slots=slots, starts=starts)
+        self.append(slots, k_new, v_new)
+        idx = self.select(q, k, sink, window, idx=idx, workspace=select_workspace) if k else None
+        out, lse = self.attend(q, idx, sink, window, scale=scale, out=out, lse=lse,
+                               workspace=workspace)
+        return idx, out, lse
 
     def check(self):
         """Synchronises and raises if a kernel recorded a device-side error."""

@@ -589,30 +589,105 @@ def test_readers_on_two_streams(rba):
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(s, sel)
 
 
-def test_long_request_split_over_every_cta(rba):
-    """20000 tokens of two heads: every unit is merged from many CTAs' parts; against torch in
-    64 bits on the rows read back."""
-    r = np.random.default_rng(5)
-    n, heads, group, dim = 20000, 2, 4, 128
-    st = rba.PagedStore(n_q_heads=8, n_kv_heads=heads, head_dim=dim, page_size=64, n_pages=320,
-                        max_requests=2, max_pages=320)
-    k, v = (cuda(rows(r, (n, heads, dim), "bf16"), "bf16") for _ in range(2))
-    slots = st.extend(i32([n - 77, 77]), n)[0]
+def test_decode_step_is_the_four_calls(rba):
+    a, b = (Pair(rba, 47, heads=2, group=2, dim=64, page=8, requests=3) for _ in range(2))
+    for p in (a, b):
+        p.grow([40, 0, 17])
+    q, qd = a.queries()
+    k, v = (cuda(rows(a.r, (5, 2, 64), "bf16"), "bf16") for _ in range(2))
+    new = i32([1, 3, 0])
+    got = a.st.decode_step(qd, k, v, new, 2, 4, 9)
+    slots, _ = b.st.extend(new, 5)
+    b.st.append(slots, k, v)
+    idx = b.st.select(qd, 2, 4, 9)
+    want = (idx, *b.st.attend(qd, idx, 4, 9))
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(a.st.pool, b.st.pool) and a.st.lens.tolist() == [41, 3, 17]
+    idx, out, lse = a.st.decode_step(qd, k[:0], v[:0], i32([0, 0, 0]), 0, 4, 9)
+    assert idx is None and torch.isfinite(out).all()
+
+
+# lines of every kind: a unit cut over many CTAs; many short units to a CTA, more than it has
+# warps; single warps with long lines; short units taken whole, more than the GPU has CTAs
+LINES = [
+    # heads, group, dim, dtype, lengths
+    (2, 4, 128, "bf16", [19923, 77]),
+    (4, 2, 64, "f32", [4000] + [16 + 5 * (i % 6) for i in range(300)]),
+    (4, 2, 64, "f32", [760] + [16 + 5 * (i % 6) for i in range(300)]),
+    (8, 4, 64, "bf16", [4500 - 13 * i for i in range(64)]),
+    (32, 1, 64, "bf16", [48000]),
+    (2, 8, 64, "f32", [90 + i % 40 for i in range(500)]),
+    (1, 6, 100, "bf16", [700 + 31 * (i % 9) for i in range(40)] + [0, 1, 31, 32, 33]),
+]
+
+
+@pytest.mark.parametrize("case", LINES)
+def test_lines_of_every_kind(rba, case):
+    """Against torch in 64 bits on the rows as held (a 32-bit store on the same pool reads them:
+    a bf16 read would round)."""
+    heads, group, dim, dtype, lens = case
+    r = np.random.default_rng(len(lens))
+    n, page = sum(lens), 64
+    shape = dict(n_q_heads=heads * group, n_kv_heads=heads, head_dim=dim, page_size=page,
+                 n_pages=sum(-(-x // page) for x in lens), max_requests=len(lens),
+                 max_pages=-(-max(lens) // page))
+    st = rba.PagedStore(**shape, dtype=dtype)
+    torch.manual_seed(len(lens))
+    k, v = (torch.randn((n, heads, dim), device="cuda").to(st.tdtype) for _ in range(2))
+    slots = st.extend(i32(lens), n)[0]
     st.append(slots, k, v)
-    q = cuda(rows(r, (2, 8, dim), "bf16"), "bf16")
-    out, lse = st.attend(q, None, 0, n)
+    q = cuda(rows(r, (len(lens), heads * group, dim), dtype), dtype)
+    ws = st.attend_workspace()
+    out, lse = st.attend(q, None, 0, max(lens), workspace=ws)
+    again = st.attend(q, None, 0, max(lens), workspace=ws)
     st.check()
-    # (values as held, in 64 bits: the bf16 read-back would round them)
-    wide = rba.PagedStore(n_q_heads=8, n_kv_heads=heads, head_dim=dim, page_size=64, n_pages=320,
-                          max_requests=2, max_pages=320, dtype="f32", pool=st.pool, rep=st.rep,
-                          table=st.table, lens=st.lens, free=st.free, n_free=st.n_free)
-    K, V = (x.double() for x in wide.read(slots))
-    for i, (a, b) in enumerate(((0, n - 77), (n - 77, n))):
-        x = torch.einsum("hgd,thd->hgt", q[i].double().view(heads, group, dim), K[a:b]) * dim ** -0.5
-        ref = torch.einsum("hgt,thd->hgd", x.softmax(-1), V[a:b]).flatten(0, 1)
-        unit = (q[i].double().abs().sum(-1).max() * K.abs().max() * dim ** -0.5 * 15 / 7).item()
-        strips = (b - a) / 16 / (64 if i == 0 else 1)  # (each of a unit's warps sums a share)
-        tol = V.abs().max().item() * (48 * unit * 2.0 ** -24 + 8 * 2.0 ** -22 + strips * 2.0 ** -23)
-        assert (out[i].double() - ref).abs().max().item() <= tol
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    wide = rba.PagedStore(**shape, dtype="f32", pool=st.pool, rep=st.rep, table=st.table,
+                          lens=st.lens, free=st.free, n_free=st.n_free)
+    K, V = wide.read(slots)
+    start = 0
+    for i, T in enumerate(lens):
+        if T == 0:
+            assert not out[i].any() and torch.isneginf(lse[i]).all()
+            continue
+        Ki, Vi = (x[start:start + T].double() for x in (K, V))
+        start += T
+        Q = q[i].double().view(heads, group, dim)
+        x = torch.einsum("hgd,thd->hgt", Q, Ki) * dim ** -0.5
+        ref = torch.einsum("hgt,thd->hgd", x.softmax(-1), Vi).flatten(0, 1)
+        unit = (Q.abs().sum(-1).max() * Ki.abs().max() * dim ** -0.5 * 15 / 7).item()
+        # at most 32 strips are summed in the matrix unit at a time
+        tol = Vi.abs().max().item() * (48 * unit * 2.0 ** -24 + 8 * 2.0 ** -22 + 32 * 2.0 ** -23)
+        assert (out[i].double() - ref).abs().max().item() <= tol, i
         want = torch.logsumexp(x, -1).flatten()
-        assert (lse[i].double() - want).abs().max().item() <= 24 * unit * 2.0 ** -24 + 16 * 2.0 ** -22
+        tol = 24 * unit * 2.0 ** -24 + (want.abs().max().item() + 4) * 2.0 ** -22
+        assert (lse[i].double() - want).abs().max().item() <= tol, i
+
+
+@pytest.mark.parametrize("heads,group,page,k,requests", [(2, 1, 16, 3, 40), (1, 3, 8, 16, 9),
+                                                         (1, 1, 4, 17, 5), (2, 2, 4, 64, 3)])
+def test_selection_of_many_rows(rba, heads, group, page, k, requests):
+    """Rows that one warp selects from and rows that a CTA does, ragged, against torch."""
+    torch.manual_seed(k)
+    lens = [(i * 977) % 3000 + i for i in range(requests)]
+    columns = -(-max(lens) // page)
+    st = rba.PagedStore(n_q_heads=heads * group, n_kv_heads=heads, head_dim=32, page_size=page,
+                        n_pages=sum(-(-n // page) for n in lens) + 1, max_requests=requests,
+                        max_pages=columns, dtype="f32")
+    st.extend(i32(lens), sum(lens))
+    st.rep[..., :32] = torch.randint(-3, 4, (st.n_pages, heads, 32), device="cuda").float()
+    q = torch.randint(-2, 3, (requests, heads * group, 32), device="cuda").float()  # many ties
+    got = st.select(q, k, 5, 33).cpu()
+    st.check()
+    Q = q.view(requests, heads, group, 32).sum(2).double().cpu()
+    rep, table = st.rep[..., :32].double().cpu(), st.table.long().cpu()
+    for i, T in enumerate(lens):
+        full = T // page
+        w0 = min(max(T - 33, 0), full * page)
+        cand = torch.arange(5 // page, max(5 // page, min(full, -(-w0 // page))))
+        for h in range(heads):
+            s = rep[table[i, cand], h] @ Q[i, h]
+            best = cand[s.sort(descending=True, stable=True).indices[:k]].sort().values
+            want = torch.full((k,), -1)
+            want[:len(best)] = best
+            assert torch.equal(got[i, h].long(), want), (i, h)
