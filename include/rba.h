@@ -516,7 +516,7 @@ typedef struct {
 /* Caller-owned device memory of a paged store. */
 typedef struct {
   void* pool;           /* as above, 16-byte aligned */
-  float* rep;           /* fp32 [n_pages][Hkv][P], 16-byte aligned: mean of each full page's stored keys */
+  float* rep;           /* fp32 [n_pages][Hkv][P], 16-byte aligned: mean stored key of full pages */
   int32_t* table;       /* [max_requests][max_pages] page numbers */
   int32_t* lens;        /* [max_requests] tokens each request holds; zeros at the start */
   int32_t* free_pages;  /* [n_pages], a stack: the first *n_free are free; all pages at the start */
@@ -578,8 +578,9 @@ rba_status rba_paged_read(const rba_paged* store, const int32_t* slots, int32_t 
  *   idx  device int32 [n_requests][Hkv][k], written: pages of the request (columns of its table
  *        row) ascending; -1 past its candidates
  *   workspace >= rba_paged_select_workspace_size() (no contents are kept in it)
- * NaN scores are not supported.  Errors: INVALID_ARG, UNSUPPORTED (more
- * than 16384 candidates in max_pages), WORKSPACE, CUDA. */
+ * Which pages a row of scores with a NaN among them selects is not specified (they are candidates
+ * all the same); other rows are not affected.  Errors: INVALID_ARG, UNSUPPORTED (more than 16384
+ * candidates in max_pages, or more than 2^31 - 1 rows), WORKSPACE, CUDA. */
 rba_status rba_paged_select(const rba_paged* store, const void* q, int64_t q_request_stride,
                             int64_t q_head_stride, int32_t n_requests, int32_t k, int32_t sink,
                             int32_t window, int32_t* idx, void* workspace, size_t ws_bytes,
@@ -588,7 +589,8 @@ size_t rba_paged_select_workspace_size(const rba_paged* store);
 
 /* Decode attention of one token of each request r < n_requests over its attended set:
  *   out = sum_t softmax_t(scale * q . k_t) v_t, lse the natural log of the sum;
- * zeros and -infinity for a request of no tokens.
+ * zeros and -infinity for a request of no tokens.  (Stored keys of 2^112 and more in size can
+ * overflow a logit's partial sums whatever q is.)
  *   idx  device int32 [n_requests][Hkv][k] as rba_paged_select writes it (NULL when k = 0): the
  *        first min(k, candidates) entries, distinct, are attended; others are not read.  An
  *        entry that is no candidate is skipped and flagged.  k = 0 with a window of at least

@@ -294,7 +294,8 @@ rba_status rba_paged_extend(rba_paged* s, const int32_t* n_new, int32_t n_reques
   a.starts = starts;
   int grid = (n_slots + kTableThreads - 1) / kTableThreads;
   grid = grid < 1 ? 1 : grid > num_sms() ? num_sms() : grid;
-  RBA_CUDA_TRY(launch_dependent(extend_kernel, static_cast<unsigned>(grid), kTableThreads, 0, stream, a));
+  RBA_CUDA_TRY(launch_dependent(extend_kernel, static_cast<unsigned>(grid), kTableThreads, 0,
+                                stream, a));
   return RBA_OK;
 }
 
@@ -307,7 +308,8 @@ rba_status rba_paged_truncate(rba_paged* s, const int32_t* keep, int32_t n_reque
   // at most a store's pages come back
   int grid = (s->d.n_pages + 4 * kTableThreads - 1) / (4 * kTableThreads);
   grid = grid > num_sms() ? num_sms() : grid;
-  RBA_CUDA_TRY(launch_dependent(truncate_kernel, static_cast<unsigned>(grid), kTableThreads, 0, stream, a));
+  RBA_CUDA_TRY(launch_dependent(truncate_kernel, static_cast<unsigned>(grid), kTableThreads, 0,
+                                stream, a));
   return RBA_OK;
 }
 

@@ -15,10 +15,10 @@
 //
 // Layout.  One warp takes a pair of strips of 16 tokens at a time.  K codes are the A operand of
 // the first product (16 tokens x 16 dims), q its B; V codes, read in token pairs, are the A operand
-// of the second (16 dims x 16 tokens), and the weights its B after 8 x 8 transposes in registers.  Up to four
-// q heads to a kv head fill the eight columns with their hi and lo halves ("packed": one product
-// for both); five to eight take a column each and a second product for the lo halves ("wide":
-// the accumulators stay 32 registers); larger groups are cut into chunks of eight.
+// of the second (16 dims x 16 tokens), and the weights its B after 8 x 8 transposes in registers.
+// Up to four q heads to a kv head fill the eight columns with their hi and lo halves ("packed": one
+// product for both); five to eight take a column each and a second product for the lo halves
+// ("wide": the accumulators stay 32 registers); larger groups are cut into chunks of eight.
 //
 // The running maximum is lazy: weights are taken relative to a reference that moves only when
 // a logit passes it by 2^4, so most strips need no cross-lane maximum and no rescale.
@@ -1041,10 +1041,12 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
   a.q_vec = reinterpret_cast<uintptr_t>(q) % (4 * dtype_size(s->d.dtype)) == 0 &&
             ((q_request_stride | q_head_stride) & 3) == 0;
   a.first = sink / a.bs;
-  // the longest unit there can be: what sink, selection and window ask for, or the whole table
-  const int64_t strips = std::min<int64_t>(
-      int64_t(sink) / kStrip + int64_t(k) * s->strips + int64_t(window) / kStrip + 4 * s->strips,
-      int64_t(s->d.max_pages) * s->strips);
+  // the longest unit there can be: what sink, selection and window ask for (each may begin and end
+  // inside a page), or the whole table
+  const auto strips_of = [&](int n) { return int64_t(n / a.bs) * s->strips + n % a.bs / kStrip; };
+  const int64_t strips =
+      std::min(strips_of(sink) + (int64_t(k) + 4) * s->strips + strips_of(window),
+               int64_t(s->d.max_pages) * s->strips);
   a.whole = (strips + 1) / 2 <= kWholePairs;
   a.by_bs = fast_div(a.bs);
   a.by_strips = fast_div(a.strips);

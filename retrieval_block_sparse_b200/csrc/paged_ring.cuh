@@ -25,8 +25,10 @@ __device__ __forceinline__ void arm_and_copy(uint32_t bar, int arm, uint32_t byt
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.s32 p, %0, 0;\n setp.ne.u32 q, %4, 0;\n"
       " @p mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%1], %2;\n"
-      " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%3], [%5], %4, [%1];\n"
-      "}\n" ::"r"(arm), "r"(bar), "r"(bytes), "r"(dst), "r"(bytes1), "l"(src)
+      " @q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%3], [%5], %4, [%1];\n}\n"
+      :
+      : "r"(arm), "r"(bar), "r"(bytes), "r"(dst), "r"(bytes1), "l"(src)
       : "memory");
 }
 // Waits, within a bound, for a phase: false when it ran out.

@@ -198,8 +198,8 @@ __device__ __forceinline__ void for_runs(const RowArgs& a, int h, int64_t base, 
     firsts &= firsts - 1;
     const int n = __ffs(~(follows >> (k + 1)));  // the first and those that follow it
     const int p = __shfl_sync(0xffffffffu, page, k), r = __shfl_sync(0xffffffffu, row, k);
-    f(base - 1 + k, n, a.pool + ((int64_t(p) * a.heads + h) * a.strips + r / kStrip) * strip_bytes(P),
-      r % kStrip);
+    const int64_t strip = (int64_t(p) * a.heads + h) * a.strips + r / kStrip;
+    f(base - 1 + k, n, a.pool + strip * strip_bytes(P), r % kStrip);
   }
 }
 

@@ -1,8 +1,8 @@
 // Paged 4-bit memory: selection of each request's best pages.
 //
 // score(r, h, j) = sum over dims of (sum over the group's q heads of q) * rep[table[r][j]][h] for
-// request r's candidate pages j, rounded once to 32 bits; the k best per (request, kv head), ties to
-// the lower page.  A 32-bit accumulation would leave the order of near pages to the order of the
+// request r's candidate pages j, rounded once to 32 bits; the k best per (request, kv head), ties
+// to the lower page.  A 32-bit accumulation would leave the order of near pages to the order of the
 // sum, so it is held in 64.  (In two 32-bit words, with exact products and sums, the same bits cost
 // a fifth more time at 86 MB of page means: five times the instructions.)
 #include "paged.cuh"
@@ -50,12 +50,13 @@ __device__ int64_t scan_batches(const SelectArgs& a, int per, int32_t* pre, int3
   return run;
 }
 
-// A warp takes a run of batches of PER candidates, through its own ring of bulk copies (a row is one
-// run of bytes): 4 KB a batch, three batches on their way, whatever the warp is computing.  (Loaded
-// into registers a batch ahead, the rows of 16 warps an SM left its memory idle half the time: 26 us
-// for 86 MB.)  The page numbers of the batch to be copied next are loaded one copy ahead.  The sums
-// are added over lanes by halving exchanges (each step halves the rows a lane carries): two or three
-// per row instead of five.
+// A warp takes a run of batches of PER candidates, through its own ring of bulk copies (a row is
+// one run of bytes): 4 KB a batch, three batches on their way, whatever the warp is computing.
+// The page numbers of the batch to be copied next are loaded one copy ahead.  The sums are added over
+// lanes by halving exchanges (each step halves the rows a lane carries): two or three per row
+// instead of five.  86 MB of page means take 21.7 us, 3.9 TB/s; with rows loaded into registers a
+// batch ahead, 16 warps an SM left the memory idle half the time (26 us).  What is left is the
+// scan of the requests before the first copy (about 4 us) and the issue slots of the 64-bit sums.
 template <typename T, int P>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(SelectArgs a) {
   constexpr int LPR = P / 4, RPW = 32 / LPR;  // lanes a row, rows a warp reads at once
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
     at.h = static_cast<int>(in / nb);
     at.c0 = static_cast<int>(in - int64_t(at.h) * nb) * PER;
   }
-  const auto advance = [&](Pos p) {  // (called where a batch is left, so a request with candidates is)
+  const auto advance = [&](Pos p) {  // (called while a batch is left: a request with candidates is)
     p.c0 += PER;
     if (p.c0 < p.nc) return p;
     p.c0 = 0;
@@ -162,7 +163,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
     double s[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const float4 x = *reinterpret_cast<const float4*>(ring + i * PLACE + (u * RPW + sub) * ROW + l * 16);
+      const float4 x =
+          *reinterpret_cast<const float4*>(ring + i * PLACE + (u * RPW + sub) * ROW + l * 16);
       s[u] = q[0] * x.x;
       s[u] = fma(q[1], double(x.y), s[u]);
       s[u] = fma(q[2], double(x.z), s[u]);
@@ -220,7 +222,8 @@ extern "C" rba_status rba_paged_select(const rba_paged* s, const void* q,
   if (k == 0) return RBA_OK;
   if (q == nullptr || idx == nullptr || workspace == nullptr) return RBA_ERR_INVALID_ARG;
   const int row = most_candidates(s, sink, window);
-  if (row > kPagedMaxCandidates) return RBA_ERR_UNSUPPORTED;
+  if (row > kPagedMaxCandidates || int64_t(n_requests) * s->d.n_kv_heads > INT32_MAX)
+    return RBA_ERR_UNSUPPORTED;
   if (ws_bytes < size_t(n_requests) * s->d.n_kv_heads * row * sizeof(float))
     return RBA_ERR_WORKSPACE;
   SelectArgs a = {};

@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kRowThreads) topk_paged_rows_kernel(
 // The same by one warp per row, for rows of up to 1024 candidates and k up to 16: the keys stay in
 // registers, and each of k rounds takes the warp's largest key, the lowest position first.  A round
 // costs about 100 instructions of one warp; a CTA's radix select costs its dozen barriers whatever k
-// is.  512 rows of up to 650 scores, k = 4: 3 us against 9; at k = 32 the CTA is the faster one.
+// is.  512 rows of up to 650 scores, k = 4: 6.3 us against 9.5 for the CTA a row; from k = 32 on the
+// CTA is the faster one.
 constexpr int kWarpRowN = 1024, kWarpRowK = 16, kWarpRowThreads = 128;
 __global__ void __launch_bounds__(kWarpRowThreads) topk_paged_warp_kernel(
     const float* __restrict__ scores, int row_stride, int rows, int heads,

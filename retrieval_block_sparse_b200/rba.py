@@ -695,6 +695,10 @@ class PagedStore:
         k_new, v_new [n][Hkv][D] (n may be larger: rows past them are ignored), then q [R][Hq][D]
         attends to sink, its k best pages and window.  Returns (idx, out, lse).  With every
         buffer given it can be captured once and replayed."""
+        n, R = k_new.shape[0], n_new.shape[0]  # (a call that is refused leaves the store as it was)
+        self._rows("k_new", k_new, n, self.Hkv)
+        self._rows("v_new", v_new, n, self.Hkv)
+        self._rows("q", q, R, self.Hq)
         slots, _ = self.extend(n_new, k_new.shape[0], slots=slots, starts=starts)
         self.append(slots, k_new, v_new)
         idx = self.select(q, k, sink, window, idx=idx, workspace=select_workspace) if k else None

@@ -396,7 +396,8 @@ def test_attention_scales(rba, scale):
     p.same_attention(q, qd, idx, sink, window, scale=scale)
 
 
-@pytest.mark.parametrize("qs,ks,vs", [(2.0 ** -60, 2.0 ** 60, 1.0), (2.0 ** 60, 2.0 ** -60, 2.0 ** 100),
+@pytest.mark.parametrize("qs,ks,vs", [(2.0 ** -60, 2.0 ** 60, 1.0),
+                                      (2.0 ** 60, 2.0 ** -60, 2.0 ** 100),
                                       (0.0, 1.0, 2.0 ** -90), (1.0, 0.0, 2.0 ** 60),
                                       (2.0 ** 10, 2.0 ** -10, 2.0 ** -60)])
 def test_attention_ranges(rba, qs, ks, vs):
@@ -452,7 +453,8 @@ def test_values_that_are_not_finite_stay_in_their_place(rba):
 def test_strided_queries(rba):
     p, idx, sink, window = _attended(rba, 29, ATTEND[0])
     q, qd = p.queries()
-    wide = torch.zeros((qd.shape[0], 3, qd.shape[1], qd.shape[2] + 8), dtype=qd.dtype, device="cuda")
+    wide = torch.zeros((qd.shape[0], 3, qd.shape[1], qd.shape[2] + 8), dtype=qd.dtype,
+                       device="cuda")
     view = wide[:, 1, :, 3:3 + qd.shape[2]]
     view.copy_(qd)
     a, b = (p.st.attend(x, i32(idx), sink, window) for x in (qd, view))
@@ -525,7 +527,7 @@ def test_decode_steps_replayed_while_requests_grow(rba):
     kv = torch.zeros((4, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
     q = torch.zeros((requests, 8, 64), dtype=torch.bfloat16, device="cuda")
     idx = torch.empty((requests, 2, k), dtype=torch.int32, device="cuda")
-    out, lse = torch.empty((requests, 8, 64), device="cuda"), torch.empty((requests, 8), device="cuda")
+    out, lse = (torch.empty((requests, 8, *d), device="cuda") for d in ((64,), ()))
     ws, sws = st.attend_workspace(), st.select_workspace()
 
     def step():
@@ -605,6 +607,35 @@ def test_decode_step_is_the_four_calls(rba):
     assert torch.equal(a.st.pool, b.st.pool) and a.st.lens.tolist() == [41, 3, 17]
     idx, out, lse = a.st.decode_step(qd, k[:0], v[:0], i32([0, 0, 0]), 0, 4, 9)
     assert idx is None and torch.isfinite(out).all()
+    for bad in ((qd[:2], k, v, new), (qd, k[:4], v, new), (qd, k, v.float(), new),
+                (qd, k, v, new.long())):
+        with pytest.raises(ValueError):
+            a.st.decode_step(*bad, 2, 4, 9)
+    assert a.st.lens.tolist() == [41, 3, 17]  # a refused step grows nothing
+    a.st.check()
+
+
+def test_keys_that_are_not_finite_leave_other_rows_alone(rba):
+    """A page mean that is not a number makes its own row's choice unspecified, no other's."""
+    for k, columns in ((3, 24), (17, 80)):  # a warp's rows, a CTA's
+        p = Pair(rba, 53, heads=2, group=2, dim=64, page=4, n_pages=120, requests=3,
+                 columns=columns)
+        keys = rows(p.r, (200, 2, 64), "bf16")
+        keys[50, 1, 7], keys[130, 0, 3] = np.nan, np.inf  # request 0 head 1, request 1 head 0
+        p.grow([90, 90, 20], pad=0, k=keys)
+        q, qd = p.queries()
+        got = p.st.select(qd, k, 0, 5).cpu().numpy()
+        p.st.check()
+        rep = p.st.rep.cpu().numpy().astype(np.float64)
+        p.m.reps = {n: np.nan_to_num(rep[n]) for n in p.m.reps}
+        want = p.m.select(q, k, 0, 5)
+        for r in range(3):
+            for h in range(2):
+                if (r, h) in ((0, 1), (1, 0)):
+                    assert len(set(got[r, h].tolist())) == k and (got[r, h] >= 0).all()
+                    assert (got[r, h] < 22).all()
+                else:
+                    assert np.array_equal(got[r, h], want[r, h]), (k, r, h)
 
 
 # lines of every kind: a unit cut over many CTAs; many short units to a CTA, more than it has
