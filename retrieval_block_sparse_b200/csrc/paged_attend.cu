@@ -47,10 +47,12 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kStages = 2;  // pairs of strips in a warp's ring (pair n takes place n % 2)
-// What a unit's start and end cost, in pairs of its worker, and the pairs that a worker takes at
-// least (or a whole unit): for CTAs and for single warps.
+// What a unit's start and end cost, in pairs of its worker: a CTA's, a single warp's; and the pairs
+// that a warp working alone takes at least (or a whole unit).  A CTA takes a multiple of kWarps, so
+// that its warps have the same number: one each at 8192 of 128K tokens (8 kv heads) takes 12.6 us,
+// two each 14.3, 18 pairs to eight warps 14.8.
 constexpr int kTeamCost = 10, kAloneCost = 3;
-constexpr int kTeamLeast = kWarps, kAloneLeast = 2;
+constexpr int kAloneLeast = 2;
 // Warps work alone where the longest unit is then cut into at most this many parts.
 constexpr int kAloneParts = 24;
 constexpr int kFold = 16;  // pairs that a warp sums in the matrix unit's accumulators
@@ -241,17 +243,19 @@ template <int P, bool kWide> struct State {
   int e;
 };
 
-template <int P, bool kWide, bool kLo>
-__device__ __forceinline__ void pair_step(const uint8_t* strips, int valid2,
-                                          const uint32_t* qw, const float* fac,
-                                          State<P, kWide>& st) {
+// One step: kN strips, whose rows `valid` holds (16 bits each).  The packed form takes a pair, for
+// one set of checks (123 us against 132, 128K tokens of 4 requests); a wide pair would be 13 KB of
+// instructions and short of registers (60.6 us against 58.9, 64 requests to 8K tokens).
+template <int P, bool kWide, bool kLo, int kN>
+__device__ __forceinline__ void strips_step(const uint8_t* strips, int valid, const uint32_t* qw,
+                                            const float* fac, State<P, kWide>& st) {
   constexpr int G = P / 32, HL = kWide ? 2 : 1, SB = strip_bytes(P);
   const int lane = threadIdx.x & 31, t = lane >> 2;
-  const bool whole = valid2 == kWholePair;
-  float y[HL][2][2];        // logits of tokens t and t + 8 of each strip for the lane's heads
-  uint32_t sv[2][2][G / 2]; // their V scales, two to a word
+  const bool whole = valid == (kN == 2 ? kWholePair : kWholeStrip);
+  float y[HL][kN][2];        // logits of tokens t and t + 8 of each strip for the lane's heads
+  uint32_t sv[kN][2][G / 2]; // their V scales, two to a word
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
+  for (int n = 0; n < kN; ++n) {
     uint32_t k[2][G], sc[2][G];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -291,11 +295,11 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid2,
   }
   if (!whole) {  // rows outside the attended set: no weight, and nothing of their scales
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < kN; ++n)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int valid = n == 0 ? valid2 & 0xffff : valid2 >> 16;
-        if (t + 8 * half >= (valid & 31) && t + 8 * half < (valid >> 5)) continue;
+        const int rows = valid >> (16 * n) & 0xffff;
+        if (t + 8 * half >= (rows & 31) && t + 8 * half < (rows >> 5)) continue;
 #pragma unroll
         for (int i = 0; i < G / 2; ++i) sv[n][half][i] = 0;
 #pragma unroll
@@ -305,14 +309,16 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid2,
   // the reference moves where a logit or a scale outgrows it
   uint32_t s2 = 0;
 #pragma unroll
-  for (int i = 0; i < 2 * 2 * (G / 2); ++i)
+  for (int i = 0; i < kN * 2 * (G / 2); ++i)
     s2 = max_bf16x2(s2, sv[i / G][(i / (G / 2)) & 1][i % (G / 2)]);
   float smax = fmaxf(bf16_of(&s2, 0), bf16_of(&s2, 1));
   bool grow = smax > st.most;
   float ymax[HL];
 #pragma unroll
   for (int i = 0; i < HL; ++i) {
-    ymax[i] = fmaxf(fmaxf(y[i][0][0], y[i][0][1]), fmaxf(y[i][1][0], y[i][1][1])) * fac[i];
+    ymax[i] = fmaxf(y[i][0][0], y[i][0][1]);
+    if constexpr (kN == 2) ymax[i] = fmaxf(ymax[i], fmaxf(y[i][kN - 1][0], y[i][kN - 1][1]));
+    ymax[i] *= fac[i];
     grow |= ymax[i] > st.top[i];
   }
   if (__any_sync(0xffffffffu, grow)) {
@@ -344,7 +350,7 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid2,
 #pragma unroll
   for (int i = 0; i < HL; ++i)
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < kN; ++n)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float p = ex2(fmaf(y[i][n][half], fac[i], -st.m[i]));
@@ -354,7 +360,7 @@ __device__ __forceinline__ void pair_step(const uint8_t* strips, int valid2,
         y[i][n][half] = p * up;
       }
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
+  for (int n = 0; n < kN; ++n) {
     uint32_t v[2][G];
 #pragma unroll
     for (int half = 0; half < 2; ++half)
@@ -547,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
   const uint32_t cost = (pairs + extra * some) * units;
   const uint32_t workers = alone ? gridDim.x * kWarps : gridDim.x;
   const uint32_t worker = alone ? blockIdx.x * kWarps + warp : blockIdx.x;
-  const uint32_t chunk =
-      max((cost + workers - 1) / workers,
-          min(longest, static_cast<uint32_t>(alone ? kAloneLeast : kTeamLeast)) + extra);
+  uint32_t chunk = (cost + workers - 1) / workers;
+  if (alone) chunk = max(chunk, min(longest, static_cast<uint32_t>(kAloneLeast)) + extra);
+  else chunk = (chunk + kWarps - 1) / kWarps * kWarps;
   if (lane == 0) s_chunk = chunk;  // (every warp the same value: its own lanes read it back)
 
   const auto at_unit = [&](int r, uint32_t u) {
@@ -651,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
                  src, me ? bytes : 0);
   };
   // q operands: one for the CTA, or a place for each of the units in its warps' lines (for each of
-  // its warps, where there are more units)
+  // its warps, where there are more units).  A unit of up to four heads is staged by one warp;
+  // eight took one warp 7 us, so those are dealt out (61.8 -> 60.8 us, 64 requests to 8K tokens).
   const auto q_place = [&](int i) {
     return reinterpret_cast<uint32_t*>(alone ? sm + S::kSlots + i * S::kSlot * 4 : sm + S::kQ);
   };
@@ -676,6 +683,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     }
   };
 
+  const auto stage_units = [&](uint32_t first, uint32_t n) {  // a warp takes one head of every unit
+    const int hh = warp;
+    const At p = unit_of(first + min(static_cast<uint32_t>(lane), n - 1));  // lane i: unit i
+    const int64_t row = p.r * a.q_req + (int64_t(p.h) * a.group + p.h0) * a.q_head;
+    float x[H][4];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const int64_t at = __shfl_sync(0xffffffffu, row, i);
+      const int nh = __shfl_sync(0xffffffffu, p.nh, i);
+      load_q(a, static_cast<const T*>(a.q) + at + hh * a.q_head,
+             i < static_cast<int>(n) && hh < nh, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      if (i >= static_cast<int>(n)) break;
+      if (hh < __shfl_sync(0xffffffffu, p.nh, i))
+        stage_q<P, kWide, kLo>(a, x[i], hh, q_place(i), fac_place(i));
+      else
+        zero_q<P, kWide, kLo>(hh, q_place(i), fac_place(i));
+    }
+  };
+
 #pragma unroll 1
   for (int n = 0; n < kStages; ++n) issue(n);
   uint32_t first_unit = 0;
@@ -684,7 +713,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     first_unit = unit_no(place(cta_begin));
     const uint32_t n = unit_no(place(cta_end - 1)) - first_unit + 1;
     shared_q = n <= kWarps;
-    if (shared_q && warp < static_cast<int>(n)) stage_all(unit_of(first_unit + warp), warp);
+    if constexpr (kWide) {
+      if (shared_q) stage_units(first_unit, n);
+    } else {
+      if (shared_q && warp < static_cast<int>(n)) stage_all(unit_of(first_unit + warp), warp);
+    }
   } else if (warp < H) {
     stage(place(begin), warp);
   }
@@ -746,9 +779,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
         // (pair j + 1 was issued last: in j's round or the next)
         const int r2 = __shfl_sync(0xffffffffu, (j & 15) == 15 && j + 1 < mine ? rows_before : rows,
                                    2 * (j & 15));
-        if (r2 != 0)
-          pair_step<P, kWide, kLo>(reinterpret_cast<const uint8_t*>(ring + (j & 1) * 2 * SB), r2,
-                                   qw, fac, st);
+        if (r2 != 0) {
+          const uint8_t* pair = reinterpret_cast<const uint8_t*>(ring + (j & 1) * 2 * SB);
+          if constexpr (kWide) {
+#pragma unroll 1
+            for (int n = 0; n < 2; ++n) {
+              const int r1 = r2 >> (16 * n) & 0xffff;
+              if (r1 != 0) strips_step<P, kWide, kLo, 1>(pair + n * SB, r1, qw, fac, st);
+            }
+          } else {
+            strips_step<P, kWide, kLo, 2>(pair, r2, qw, fac, st);
+          }
+        }
         __syncwarp();
         issue(j + kStages);
       }
