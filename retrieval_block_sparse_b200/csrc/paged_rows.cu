@@ -28,7 +28,7 @@ struct RowArgs {
   int32_t* status;
   int n, heads, dim, bs, strips, n_pages;
   int window;  // slots a CTA looks for runs in
-  FastDiv by_bs, by_heads;
+  FastDiv by_bs, by_heads, by_chunks;
   bool vec;    // every row starts on a boundary of four elements
 };
 
@@ -40,11 +40,26 @@ template <> struct Four<float> {
   __device__ __forceinline__ void load(const float* p, bool vec) { load4(p, vec, x); }
   __device__ __forceinline__ void zero() { x[0] = x[1] = x[2] = x[3] = 0.f; }
   __device__ __forceinline__ float operator[](int i) const { return x[i]; }
-  __device__ __forceinline__ uint32_t top() const {
-    uint32_t m = 0;
+  // of eight rows over the eight lanes of a group, row l to lane l: after the step of width w a
+  // lane keeps the w rows that share its bit w
+  static __device__ __forceinline__ uint32_t top(const Four* r, int l) {
+    uint32_t m[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-    return m;
+    for (int j = 0; j < 8; ++j) {
+      m[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[j] = max(m[j], __float_as_uint(r[j].x[i]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int w = 4; w > 0; w >>= 1) {
+      const bool up = (l & w) != 0;
+#pragma unroll
+      for (int j = 0; j < w; ++j) {
+        const uint32_t give = up ? m[j] : m[j + w], keep = up ? m[j + w] : m[j];
+        m[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, w));
+      }
+    }
+    return m[0];
   }
 };
 template <> struct Four<__nv_bfloat16> {
@@ -63,63 +78,92 @@ template <> struct Four<__nv_bfloat16> {
     const uint32_t w = i < 2 ? u.x : u.y;
     return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
   }
-  __device__ __forceinline__ uint32_t top() const {
-    const uint32_t m = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu);
-    return max(m << 16, m & 0xffff0000u);
+  // the same with two rows to a word
+  static __device__ __forceinline__ uint32_t top(const Four* r, int l) {
+    uint32_t m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = __vmaxu2(r[2 * j].u.x & 0x7fff7fffu, r[2 * j].u.y & 0x7fff7fffu);
+      const uint32_t b = __vmaxu2(r[2 * j + 1].u.x & 0x7fff7fffu, r[2 * j + 1].u.y & 0x7fff7fffu);
+      m[j] = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    }
+#pragma unroll
+    for (int w = 2; w > 0; w >>= 1) {
+      const bool up = (l & (2 * w)) != 0;
+#pragma unroll
+      for (int j = 0; j < w; ++j) {
+        const uint32_t give = up ? m[j] : m[j + w], keep = up ? m[j + w] : m[j];
+        m[j] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, give, 2 * w));
+      }
+    }
+    m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+    return l & 1 ? m[0] & 0xffff0000u : m[0] << 16;
   }
 };
-__device__ __forceinline__ void store4(float* p, const float* x) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
-  __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-  uint2 u;
-  u.x = *reinterpret_cast<uint32_t*>(&a);
-  u.y = *reinterpret_cast<uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
-}
-
 // A group's scale and the factor of its codes (0 where the codes are all 0) from the bits of its
-// largest |x| (as integers, values that are not finite are the largest).
-__device__ __forceinline__ void scale_of_max(uint32_t bits, uint16_t* scale, float* inv) {
+// largest |x|; whether it holds a value that is not finite.
+__device__ __forceinline__ bool scale_of_max(uint32_t bits, uint16_t* scale, float* inv) {
   const __nv_bfloat16 s = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(bits), 7.f));
   const float sf = __bfloat162float(s);
   const bool odd = bits >= 0x7f800000u, none = sf < kLeastScale;
   *scale = odd ? 0x7fff : none ? 0 : __bfloat16_as_ushort(s);
   *inv = odd || none ? 0.f : __frcp_rn(sf);
+  return odd;
 }
-// Four codes, one 16-bit unit.  |x| inv <= 7 (1 + 2^-8) rounds to 7 at most: no clamp is needed.
+// Four codes, one 16-bit unit (of finite x).  |x| inv <= 7 (1 + 2^-8) rounds to 7 at most: no clamp
+// is needed.
 template <typename R>
 __device__ __forceinline__ uint32_t unit_of(const R& x, float inv) {
   uint32_t b[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[j], inv), kToInt));
-  const uint32_t u = (b[0] + (b[1] << 4) + (b[2] << 8) + (b[3] << 12)) & 0xffffu;
-  return inv == 0.f ? 0x8888u : u;
+  return (b[0] + (b[1] << 4) + (b[2] << 8) + (b[3] << 12)) & 0xffffu;
 }
-// c of the low nibble c + 8: as the low bits of 2^23 + c + 8
-__device__ __forceinline__ float code_of(uint32_t nibble) {
-  return __uint_as_float((nibble & 15u) | 0x4b000000u) - 8388616.f;
+// c of nibble J < 5 of a word: left in its place as the low bits of 2^(23 - 4 J) + c + 8, less that
+template <int J> __device__ __forceinline__ float code_of(uint32_t w) {
+  static_assert(J < 5, "the nibble lies in a float's 23 bits");
+  constexpr float base = float(1 << (23 - 4 * J));
+  return __uint_as_float((w & (15u << (4 * J))) | uint32_t(150 - 4 * J) << 23) - (base + 8.f);
 }
-__device__ __forceinline__ void values4(uint32_t unit, float s, float* x) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    x[j] = __fmul_rn(code_of(unit >> (4 * j)), s);
+__device__ __forceinline__ void codes8(uint32_t w, float* x) {
+  const uint32_t u = w >> 16;
+  x[0] = code_of<0>(w); x[1] = code_of<1>(w); x[2] = code_of<2>(w); x[3] = code_of<3>(w);
+  x[4] = code_of<0>(u); x[5] = code_of<1>(u); x[6] = code_of<2>(u); x[7] = code_of<3>(u);
+}
+// The four values of a 16-bit unit and its bf16 scale, to a row.  (A product of a code and a scale
+// is exact in 32 bits, and rounded once to bf16 either way.)
+__device__ __forceinline__ void store_values(float* p, uint32_t unit, uint32_t scale) {
+  const float s = __uint_as_float(scale << 16);
+  *reinterpret_cast<float4*>(p) = make_float4(
+      __fmul_rn(code_of<0>(unit), s), __fmul_rn(code_of<1>(unit), s),
+      __fmul_rn(code_of<2>(unit), s), __fmul_rn(code_of<3>(unit), s));
+}
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t unit, uint32_t scale) {
+  const uint32_t y = unit | unit << 12, s2 = scale | scale << 16;  // nibbles 1 and 3 above 0 and 2
+  const auto two = [&](uint32_t w) {  // as the low bits of 128 + c + 8, twice
+    const uint32_t n = (w & 0x000f000fu) | 0x43004300u, off = 0xc308c308u;
+    const __nv_bfloat162 c = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&n),
+                                        *reinterpret_cast<const __nv_bfloat162*>(&off));
+    const __nv_bfloat162 v = __hmul2_rn(c, *reinterpret_cast<const __nv_bfloat162*>(&s2));
+    return *reinterpret_cast<const uint32_t*>(&v);
+  };
+  *reinterpret_cast<uint2*>(p) = make_uint2(two(y), two(y >> 8));
 }
 
 // Quantises eight tokens' K or V rows of one strip: tokens [t0, t0 + n) of the strip are slots
 // i0 .. of the call, head h; this warp takes those of half `half`.  Lane (g, l) holds four dims of
 // each row (P = 64: K in one half of the warp, V in the other).  The rows' largest values are
-// found by halving exchanges that leave row l with lane l, so that the division and the reciprocal
-// are computed once per group.  Everything goes to `to`, the strip or its copy in shared memory;
-// v_pairs: the tokens' V units can be written two at a time.
-template <typename T, int P>
+// found by exchanges that leave row l with lane l, so that the division and the reciprocal are
+// computed once per group.  A whole strip (kWhole: t0 = 0, n = 16) goes to its copy in shared
+// memory, and its tokens' V units are written two at a time.
+template <typename T, int P, bool kWhole>
 __device__ __forceinline__ void write_half(const RowArgs& a, int64_t i0, int h, int t0, int n,
-                                           int which, int half, uint8_t* to, bool v_pairs) {
+                                           int which, int half, uint8_t* to) {
   constexpr int LPR = P / 4;
   const int lane = threadIdx.x & 31, sub = lane % LPR, g = sub / 8, l = sub % 8;
-  const int first = half * 8 - t0;  // run index of the half's token 0
-  if (first + 8 <= 0 || first >= n) return;
+  const int first = kWhole ? half * 8 : half * 8 - t0;  // run index of the half's token 0
+  if (!kWhole && (first + 8 <= 0 || first >= n)) return;
+  const auto there = [&](int j) { return kWhole || (first + j >= 0 && first + j < n); };
   const T* base = which == 0 ? static_cast<const T*>(a.k) + i0 * a.k_tok + h * a.k_head
                              : static_cast<const T*>(a.v) + i0 * a.v_tok + h * a.v_head;
   const int64_t step = which == 0 ? a.k_tok : a.v_tok;
@@ -127,33 +171,24 @@ __device__ __forceinline__ void write_half(const RowArgs& a, int64_t i0, int h, 
   const T* p = base + first * step + sub * 4;
 #pragma unroll
   for (int j = 0; j < 8; ++j, p += step) {
-    const int i = first + j;
-    if (i >= 0 && i < n && sub * 4 < a.dim) x[j].load(p, a.vec);
+    if (there(j) && sub * 4 < a.dim) x[j].load(p, a.vec);
     else x[j].zero();
-  }
-  uint32_t m[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = x[j].top();
-  // halving: after the step of width w a lane keeps the w rows that share its bit w
-#pragma unroll
-  for (int w = 4; w > 0; w >>= 1) {
-    const bool up = (l & w) != 0;
-#pragma unroll
-    for (int j = 0; j < w; ++j) {
-      const uint32_t give = up ? m[j] : m[j + w], keep = up ? m[j + w] : m[j];
-      m[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, w));
-    }
   }
   uint16_t scale;
   float inv;
-  scale_of_max(m[0], &scale, &inv);
-  if (first + l >= 0 && first + l < n)
-    *reinterpret_cast<uint16_t*>(to + scale_at<P>(half * 8 + l, which, g)) = scale;
+  const bool odd = scale_of_max(Four<T>::top(x, l), &scale, &inv);
+  if (there(l)) *reinterpret_cast<uint16_t*>(to + scale_at<P>(half * 8 + l, which, g)) = scale;
   uint32_t unit[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     unit[j] = unit_of(x[j], __shfl_sync(0xffffffffu, inv, (lane & 24) + j));
-  if (v_pairs && which == 1) {
+  const unsigned odds = __ballot_sync(0xffffffffu, odd) >> (lane & 24);
+  if (odds) {  // (a row of such values has codes 0)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (odds >> j & 1) unit[j] = 0x8888u;
+  }
+  if (kWhole && which == 1) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<uint32_t*>(to + v_unit_at<P>(half * 8 + 2 * c, g, l)) =
@@ -162,7 +197,7 @@ __device__ __forceinline__ void write_half(const RowArgs& a, int64_t i0, int h, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int t = half * 8 + j;
-      if (first + j >= 0 && first + j < n)
+      if (there(j))
         *reinterpret_cast<uint16_t*>(
             to + (which == 0 ? k_unit_at<P>(t, g, l) : v_unit_at<P>(t, g, l))) =
             static_cast<uint16_t>(unit[j]);
@@ -219,9 +254,11 @@ __global__ void __launch_bounds__(run_warps<P>() * 32,
   const int which = P == 128 ? warp >> 1 : lane >> 4, half = warp & 1;
   const int w = div(blockIdx.x, a.by_heads), h = blockIdx.x - w * a.heads;
   for_runs<P>(a, h, int64_t(w) * a.window, [&](int64_t i0, int n, uint8_t* strip, int t0) {
-    const bool whole = n == kStrip;
-    write_half<T, P>(a, i0, h, t0, n, which, half, whole ? s_stage : strip, whole);
-    if (!whole) return;
+    if (n != kStrip) {
+      write_half<T, P, false>(a, i0, h, t0, n, which, half, strip);
+      return;
+    }
+    write_half<T, P, true>(a, i0, h, 0, n, which, half, s_stage);
     __syncthreads();
     for (int o = threadIdx.x * 16; o < SB; o += kThreads * 16)
       *reinterpret_cast<uint4*>(strip + o) = *reinterpret_cast<const uint4*>(s_stage + o);
@@ -229,70 +266,88 @@ __global__ void __launch_bounds__(run_warps<P>() * 32,
   });
 }
 
-// Means of the pages whose last row is among the slots: one CTA per (32 slots, head), its warps
-// each a share of a page's strips.  Lane (t, c) sums rows t and t + 8 over dims 8 c .. + 7 of each
-// group; halving exchanges add the eight lanes of a c and leave G values with each; the warps' sums
-// are added in order.
-constexpr int kMeanWarps = 8;
+// Means of the pages whose last row is among the slots: one CTA per (`words` x 32 slots, head).
+// Its warps find the pages, each for itself, and take them in groups of as many warps as a page has
+// strips (the next power of two; all eight where there are more).  A lane holds one word of every second
+// row (P = 64: every fourth), dims 32 g + 8 c .. + 7, so that its sums meet one other lane's (three
+// others') in the end; the warps' sums are added in order.
+constexpr int kMeanWarps = 8, kMeanWords = 4;  // up to 4 words of 32 slots
 template <int P>
-__global__ void __launch_bounds__(kMeanWarps * 32) page_mean_kernel(RowArgs a) {
+__global__ void __launch_bounds__(kMeanWarps * 32) page_mean_kernel(RowArgs a, int words,
+                                                                    int log_warps) {
   constexpr int G = P / 32, SB = strip_bytes(P);
-  __shared__ float s_sum[kMeanWarps][P];
+  constexpr int WORDS = 4 * G;                            // of a row
+  constexpr int ROWS = 32 / WORDS, ITER = kStrip / ROWS;  // of a load; loads of a strip
+  __shared__ __align__(16) float s_sum[kMeanWarps][P];
   wait_for_stream();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane >> 2, c = lane & 3;
-  const int w32 = div(blockIdx.x, a.by_heads), h = blockIdx.x - w32 * a.heads;
-  const int64_t i = int64_t(w32) * 32 + lane;
-  const int mine = i < a.n ? a.slots[i] : -1;
-  const int at = mine >= 0 ? div(mine, a.by_bs) : 0;
-  unsigned done = __ballot_sync(
-      0xffffffffu, mine >= 0 && at < a.n_pages && mine - at * a.bs == a.bs - 1);
-  for (; done; done &= done - 1) {
-    const int page = __shfl_sync(0xffffffffu, at, __ffs(done) - 1);
-    const uint8_t* strips = a.pool + (int64_t(page) * a.heads + h) * a.strips * SB;
-    float acc[8 * G];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = lane % WORDS / G, g = lane % G;
+  const int window = div(blockIdx.x, a.by_heads), h = blockIdx.x - window * a.heads;
+  int at[kMeanWords];  // the page that a slot completes, or -1; those before it in the window
+  int before[kMeanWords], count = 0;
 #pragma unroll
-    for (int e = 0; e < 8 * G; ++e) acc[e] = 0.f;
-    for (int s = warp; s < a.strips; s += kMeanWarps) {
-      const uint8_t* strip = strips + int64_t(s) * SB;
+  for (int w = 0; w < kMeanWords; ++w) {
+    const int64_t i = (int64_t(window) * words + w) * 32 + lane;
+    at[w] = w < words && i < a.n ? a.slots[i] : -1;
+  }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t word[G];
-        float sc[G];
+  for (int w = 0; w < kMeanWords; ++w) {
+    const int page = at[w] >= 0 ? div(at[w], a.by_bs) : 0;
+    const bool last = at[w] >= 0 && page < a.n_pages && at[w] - page * a.bs == a.bs - 1;
+    at[w] = last ? page : -1;
+    const unsigned done = __ballot_sync(0xffffffffu, last);
+    before[w] = last ? count + __popc(done & ((1u << lane) - 1)) : -1;
+    count += __popc(done);
+  }
+  const int warps_a_page = 1 << log_warps, pages_at_once = kMeanWarps >> log_warps;
+  const int group = warp >> log_warps, in_group = warp & (warps_a_page - 1);
+  for (int p0 = 0; p0 < count; p0 += pages_at_once) {
+    int page = -1;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {  // (a strip's rows past the page exist: loaded, not added)
-          word[g] = reinterpret_cast<const uint32_t*>(strip + half * 4 * P + lane * (G * 4))[g];
-          sc[g] = __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(
-                                      strip + scale_at<P>(half * 8 + t, 0, 0))[g]) << 16);
+    for (int w = 0; w < kMeanWords; ++w) {
+      const unsigned it = __ballot_sync(0xffffffffu, before[w] == p0 + group);
+      if (it) page = __shfl_sync(0xffffffffu, at[w], __ffs(it) - 1);
+    }
+    if (page >= 0) {
+      const uint8_t* strips = a.pool + (int64_t(page) * a.heads + h) * a.strips * SB;
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int s = in_group; s < a.strips; s += warps_a_page) {
+        const uint8_t* strip = strips + int64_t(s) * SB;
+        uint32_t word[ITER];
+        float sc[ITER];
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {  // (a strip's rows past the page exist: loaded, not added)
+          const int t = i * ROWS + lane / WORDS;
+          word[i] = reinterpret_cast<const uint32_t*>(strip)[i * 32 + lane];
+          sc[i] = __uint_as_float(
+              uint32_t(*reinterpret_cast<const uint16_t*>(strip + scale_at<P>(t, 0, g))) << 16);
         }
-        if (s * kStrip + half * 8 + t >= a.bs) continue;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
+        for (int i = 0; i < ITER; ++i) {
+          if (s * kStrip + i * ROWS + lane / WORDS >= a.bs) continue;
+          float x[8];
+          codes8(word[i], x);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            acc[8 * g + j] = fmaf(code_of(word[g] >> (4 * j)), sc[g], acc[8 * g + j]);
+          for (int j = 0; j < 8; ++j) acc[j] = fmaf(x[j], sc[i], acc[j]);
+        }
       }
-    }
-    // lane (t, c) ends with values G t .. of its c's 8 G
 #pragma unroll
-    for (int w = 4; w > 0; w >>= 1) {
-      const bool up = (t & w) != 0;
+      for (int o = WORDS; o < 32; o <<= 1)
 #pragma unroll
-      for (int e = 0; e < G * w; ++e) {
-        const float give = up ? acc[e] : acc[e + G * w], keep = up ? acc[e + G * w] : acc[e];
-        acc[e] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * w);
+        for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+      if (lane < WORDS) {
+        float4* to = reinterpret_cast<float4*>(&s_sum[warp][32 * g + 8 * c]);
+        to[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        to[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
       }
-    }
-#pragma unroll
-    for (int e = 0; e < G; ++e) {
-      const int v = G * t + e;  // of (group, dim) = (v / 8, v % 8)
-      s_sum[warp][32 * (v / 8) + 8 * c + v % 8] = acc[e];
     }
     __syncthreads();
-    if (threadIdx.x < P) {
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kMeanWarps; ++w) sum += s_sum[w][threadIdx.x];
-      a.rep[(int64_t(page) * a.heads + h) * P + threadIdx.x] = sum / static_cast<float>(a.bs);
+    if (page >= 0) {
+      for (int d = in_group * 32 + lane; d < P; d += warps_a_page * 32) {
+        float sum = 0.f;
+        for (int w = 0; w < warps_a_page; ++w) sum += s_sum[group * warps_a_page + w][d];
+        a.rep[(int64_t(page) * a.heads + h) * P + d] = sum / static_cast<float>(a.bs);
+      }
     }
     __syncthreads();
   }
@@ -306,43 +361,43 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(RowArgs a) {
   constexpr int LPR = P / 4, SB = strip_bytes(P);
   wait_for_stream();
   const int lane = threadIdx.x & 31, sub = lane % LPR, g = sub / 8, l = sub % 8;
-  const int64_t w = int64_t(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
-  const int chunks = (a.heads + kHeads - 1) / kHeads;
-  const int64_t i = w / chunks;
-  const int h0 = static_cast<int>(w - i * chunks) * kHeads;
+  const int w = blockIdx.x * kReadWarps + (threadIdx.x >> 5), i = div(w, a.by_chunks);
+  const int h0 = (w - i * a.by_chunks.d) * kHeads;
   if (i >= a.n) return;
   const int slot = a.slots[i];
   const int page = slot >= 0 ? div(slot, a.by_bs) : 0, row = slot - page * a.bs, t = row % kStrip;
   const bool in = slot >= 0 && page < a.n_pages;
   if (slot >= 0 && !in && lane == 0 && h0 == 0) report(a.status, RBA_ERR_BOUNDS, kWherePaged, slot);
   if (sub * 4 >= a.dim) return;
-  uint32_t unit[kHeads][2];
-  uint16_t scale[kHeads][2];
+  const int64_t head_bytes = int64_t(a.strips) * SB;
+  const uint8_t* strip =
+      a.pool + (int64_t(in ? page : 0) * a.heads + h0) * head_bytes + (in ? row / kStrip : 0) * SB;
+  const int64_t out = (int64_t(i) * a.heads + h0) * a.dim + sub * 4;
+  // the lane's unit and scale in a strip: of K and V in turn, or (P = 64) of its half warp's one
+  constexpr int kPasses = 2 * LPR / 32;
+  const int which0 = P == 128 ? 0 : lane / LPR;
+  uint32_t unit[kHeads][kPasses], scale[kHeads][kPasses];
 #pragma unroll
   for (int j = 0; j < kHeads; ++j)
 #pragma unroll
-    for (int pass = 0; pass < 2 * LPR / 32; ++pass) {
+    for (int pass = 0; pass < kPasses; ++pass) {
+      const int which = which0 + pass;
       unit[j][pass] = 0x8888u;
       scale[j][pass] = 0;
-      if (!in || h0 + j >= a.heads) continue;
-      const int which = P == 128 ? pass : lane / LPR;
-      const uint8_t* strip =
-          a.pool + ((int64_t(page) * a.heads + h0 + j) * a.strips + row / kStrip) * SB;
-      unit[j][pass] = *reinterpret_cast<const uint16_t*>(
-          strip + (which == 0 ? k_unit_at<P>(t, g, l) : v_unit_at<P>(t, g, l)));
-      scale[j][pass] = *reinterpret_cast<const uint16_t*>(strip + scale_at<P>(t, which, g));
+      if (in && (j == 0 || h0 + j < a.heads)) {
+        const uint8_t* p = strip + j * head_bytes;
+        unit[j][pass] = *reinterpret_cast<const uint16_t*>(
+            p + (which == 0 ? k_unit_at<P>(t, g, l) : v_unit_at<P>(t, g, l)));
+        scale[j][pass] = *reinterpret_cast<const uint16_t*>(p + scale_at<P>(t, which, g));
+      }
     }
 #pragma unroll
   for (int j = 0; j < kHeads; ++j)
 #pragma unroll
-    for (int pass = 0; pass < 2 * LPR / 32; ++pass) {
-      if (h0 + j >= a.heads) continue;
-      const int which = P == 128 ? pass : lane / LPR;
-      float x[4];
-      values4(unit[j][pass], __uint_as_float(uint32_t(scale[j][pass]) << 16), x);
-      store4(static_cast<T*>(which == 0 ? a.k_out : a.v_out) +
-                 (i * a.heads + h0 + j) * a.dim + sub * 4, x);
-    }
+    for (int pass = 0; pass < kPasses; ++pass)
+      if (j == 0 || h0 + j < a.heads)
+        store_values(static_cast<T*>(which0 + pass == 0 ? a.k_out : a.v_out) + out + j * a.dim,
+                     unit[j][pass], scale[j][pass]);
 }
 
 RowArgs row_args(const rba_paged* s, const int32_t* slots, int n) {
@@ -394,12 +449,17 @@ extern "C" rba_status rba_paged_append(rba_paged* s, const int32_t* slots, int32
           ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 3) == 0;
   const unsigned grid = run_grid(a, a.window);
   if (grid == 0) return RBA_ERR_UNSUPPORTED;
+  // means: 128 slots a CTA, fewer where that would leave SMs without two (8192 tokens of 8 heads:
+  // 24.9 us with their read-back, 25.8 with 64 slots; 777 of 32 heads: 20.2 and 18.8)
+  int words = kMeanWords, log_warps = 0;  // (log_warps: of a page's warps)
+  while (words > 1 && run_grid(a, words * 32) < 2u * num_sms()) words /= 2;
+  while (1 << log_warps < kMeanWarps && 1 << log_warps < a.strips) ++log_warps;
 #define RBA_APPEND(T_, P_)                                                                      \
   do {                                                                                          \
     RBA_CUDA_TRY(launch_dependent(append_kernel<T_, P_>, grid, run_warps<P_>() * 32, 0, stream, \
                                   a));                                                          \
-    RBA_CUDA_TRY(launch_dependent(page_mean_kernel<P_>, run_grid(a, 32), kMeanWarps * 32, 0,    \
-                                  stream, a));                                                  \
+    RBA_CUDA_TRY(launch_dependent(page_mean_kernel<P_>, run_grid(a, words * 32),                \
+                                  kMeanWarps * 32, 0, stream, a, words, log_warps));            \
   } while (0)
   if (s->d.dtype == RBA_BF16) {
     if (s->pitch == 128) RBA_APPEND(__nv_bfloat16, 128);
@@ -423,9 +483,10 @@ extern "C" rba_status rba_paged_read(const rba_paged* s, const int32_t* slots, i
   RowArgs a = row_args(s, slots, n);
   a.k_out = k;
   a.v_out = v;
-  const int64_t grid =
-      (int64_t(n) * ((a.heads + kHeads - 1) / kHeads) + kReadWarps - 1) / kReadWarps;
-  if (grid > INT32_MAX) return RBA_ERR_UNSUPPORTED;
+  const int chunks = (a.heads + kHeads - 1) / kHeads;
+  const int64_t grid = (int64_t(n) * chunks + kReadWarps - 1) / kReadWarps;
+  if (grid * kReadWarps > INT32_MAX) return RBA_ERR_UNSUPPORTED;
+  a.by_chunks = fast_div(chunks);
   const auto kernel = s->d.dtype == RBA_BF16
                           ? (s->pitch == 128 ? read_kernel<__nv_bfloat16, 128>
                                              : read_kernel<__nv_bfloat16, 64>)

@@ -241,6 +241,35 @@ def test_special_values(rba):
     assert np.isnan(want[1, 32:64]).all() and np.isfinite(want[1, :32]).all()
 
 
+@pytest.mark.parametrize("heads,dim,page,tokens", [(1, 64, 1, 300), (3, 128, 2, 1000),
+                                                   (40, 128, 17, 900), (2, 96, 33, 777),
+                                                   (8, 64, 200, 5000)])
+def test_means_of_every_page_that_a_call_completes(rba, heads, dim, page, tokens):
+    """Few and many pages to a CTA, of one strip to thirteen; an open last page keeps its mean."""
+    st = rba.PagedStore(n_q_heads=heads, n_kv_heads=heads, head_dim=dim, page_size=page,
+                        n_pages=tokens // page + 2, max_requests=2, max_pages=tokens // page + 2)
+    torch.manual_seed(page)
+    slots = st.extend(i32([tokens // 3, tokens - tokens // 3]), tokens)[0]
+    k = torch.randn((tokens, heads, dim), device="cuda").bfloat16()
+    st.rep.fill_(7.0)
+    st.append(slots, k, k)
+    wide = rba.PagedStore(n_q_heads=heads, n_kv_heads=heads, head_dim=dim, page_size=page,
+                          n_pages=st.n_pages, max_requests=2, max_pages=st.max_pages, dtype="f32",
+                          pool=st.pool, rep=st.rep, table=st.table, lens=st.lens, free=st.free,
+                          n_free=st.n_free)
+    rows = wide.read(torch.arange(st.n_pages * page, dtype=torch.int32, device="cuda"))[0]
+    rows = rows.view(st.n_pages, page, heads, dim).double()
+    used = torch.zeros(st.n_pages, dtype=torch.bool)
+    for r, n in enumerate((tokens // 3, tokens - tokens // 3)):
+        used[st.table[r, :n // page].cpu().long()] = True
+    want, got = rows.mean(1), st.rep[..., :dim].double()
+    # page - 1 sums, each rounded to half a step of at most the sum of |x|; the products are exact,
+    # the division adds one more
+    tol = rows.abs().sum(1) * 2.0 ** -24 * (page + 1) / page
+    assert ((got - want).abs()[used] <= tol[used]).all()
+    assert (st.rep[~used] == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f32", 100), ("bf16", 36)])
 def test_strided_rows(rba, dtype, dim):
     # slices of a fused projection, an odd head stride, a view that starts off a boundary
