@@ -81,9 +81,14 @@ __host__ __device__ inline int paged_w0(int T, int full, int bs, int window) {
   const int open = T > window ? T - window : 0;
   return open < full * bs ? open : full * bs;
 }
-__host__ __device__ inline PagedGeo paged_geo(int T, int bs, int sink, int window) {
+inline PagedGeo paged_geo(int T, int bs, int sink, int window) {
   const int full = T / bs;
   return paged_geo(T, full, paged_w0(T, full, bs, window) / bs, sink / bs, bs, sink, window);
+}
+__device__ __forceinline__ PagedGeo paged_geo(int T, const FastDiv& by_bs, int first, int sink,
+                                              int window) {
+  const int bs = by_bs.d, full = div(T, by_bs);
+  return paged_geo(T, full, div(paged_w0(T, full, bs, window), by_bs), first, bs, sink, window);
 }
 
 // A request's length as the store holds it; a length outside the table is reported and

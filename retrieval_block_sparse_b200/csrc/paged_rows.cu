@@ -268,9 +268,9 @@ __global__ void __launch_bounds__(run_warps<P>() * 32,
 
 // Means of the pages whose last row is among the slots: one CTA per (`words` x 32 slots, head).
 // Its warps find the pages, each for itself, and take them in groups of as many warps as a page has
-// strips (the next power of two; all eight where there are more).  A lane holds one word of every second
-// row (P = 64: every fourth), dims 32 g + 8 c .. + 7, so that its sums meet one other lane's (three
-// others') in the end; the warps' sums are added in order.
+// strips (the next power of two; all eight where there are more).  A lane holds one word of every
+// second row (P = 64: every fourth), dims 32 g + 8 c .. + 7, so that its sums meet one other lane's
+// (three others') in the end; the warps' sums are added in order.
 constexpr int kMeanWarps = 8, kMeanWords = 4;  // up to 4 words of 32 slots
 template <int P>
 __global__ void __launch_bounds__(kMeanWarps * 32) page_mean_kernel(RowArgs a, int words,

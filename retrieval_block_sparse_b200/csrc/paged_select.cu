@@ -25,26 +25,28 @@ struct SelectArgs {
   int32_t* status;
   float* scores;  // [R][Hkv][row]
   int R, heads, group, dim, bs, max_pages, n_pages, sink, window, row;
+  int first;   // sink / bs
   bool q_vec;  // rows of q start on a boundary of four elements
+  FastDiv by_bs, by_heads, by_warps;  // (warps of the grid)
 };
 
 // pre[r] = batches of `per` candidates of the requests before r (one kv head); returns their sum.
-__device__ int64_t scan_batches(const SelectArgs& a, int per, int32_t* pre, int32_t* ncand,
+__device__ int scan_batches(const SelectArgs& a, int per, int32_t* pre, int32_t* ncand,
                                 int64_t* s_w) {
-  int64_t run = 0;
+  int run = 0;
   for (int base = 0; base < a.R; base += blockDim.x) {
     const int r = base + threadIdx.x;
     int nb = 0;
     if (r < a.R) {
       const int T = paged_len(a.lens, r, a.bs, a.max_pages, a.status);
-      const PagedGeo g = paged_geo(T, a.bs, a.sink, a.window);
+      const PagedGeo g = paged_geo(T, a.by_bs, a.first, a.sink, a.window);
       ncand[r] = g.nc;
       nb = (g.nc + per - 1) / per;
     }
     int64_t tot;
     const int64_t ex = block_scan64(nb, s_w, &tot);
-    if (r < a.R) pre[r] = static_cast<int32_t>(run + ex);
-    run += tot;
+    if (r < a.R) pre[r] = run + static_cast<int>(ex);
+    run += static_cast<int>(tot);
   }
   __syncthreads();
   return run;
@@ -52,11 +54,12 @@ __device__ int64_t scan_batches(const SelectArgs& a, int per, int32_t* pre, int3
 
 // A warp takes a run of batches of PER candidates, through its own ring of bulk copies (a row is
 // one run of bytes): 4 KB a batch, three batches on their way, whatever the warp is computing.
-// The page numbers of the batch to be copied next are loaded one copy ahead.  The sums are added over
-// lanes by halving exchanges (each step halves the rows a lane carries): two or three per row
-// instead of five.  86 MB of page means take 21.7 us, 3.9 TB/s; with rows loaded into registers a
-// batch ahead, 16 warps an SM left the memory idle half the time (26 us).  What is left is the
-// scan of the requests before the first copy (about 4 us) and the issue slots of the 64-bit sums.
+// The page numbers of the batch to be copied next are loaded one copy ahead.  The sums are added
+// over lanes by halving exchanges (each step halves the rows a lane carries): two or three per row
+// instead of five.  86 MB of page means and the choice among them take 28.1 us, the means alone
+// about 20 (4.3 TB/s); with rows loaded into registers a batch ahead, 16 warps an SM left the memory
+// idle half the time (26 us for the means).  What is left is the scan of the requests before the
+// first copy (about 4 us) and the latency and issue slots of the 64-bit sums.
 template <typename T, int P>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(SelectArgs a) {
   constexpr int LPR = P / 4, RPW = 32 / LPR;  // lanes a row, rows a warp reads at once
@@ -72,25 +75,24 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   wait_for_stream();
-  const int64_t one = scan_batches(a, PER, pre, ncand, s_w);
+  const int one = scan_batches(a, PER, pre, ncand, s_w);
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const int first = a.sink / a.bs;
-  const int64_t all = one * a.heads;
-  const int64_t nw = int64_t(gridDim.x) * (kScoreThreads / 32);
-  // (warps of one CTA lie far apart, so that few batches use every SM)
-  const int64_t w = int64_t(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-  const int64_t b0 = all * w / nw, b1 = all * (w + 1) / nw;
-  if (b0 >= b1) return;
+  // the warp's share of all batches (warps of one CTA lie far apart, so that few batches use every
+  // SM).  With 64-bit and plain divisions here a selection over 86 MB took 30.1 us, not 28.1.
+  const int all = one * a.heads, w = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  const int share = div(all, a.by_warps), more = all - share * static_cast<int>(a.by_warps.d);
+  const int b0 = w * share + min(w, more), batches = share + (w < more);
+  if (batches == 0) return;
   struct Pos {
     int r, h, c0, nc;  // request, kv head, first candidate of the batch, the request's candidates
   } at;
-  at.r = last_at_most(pre, a.R, static_cast<int32_t>(b0 / a.heads));
+  at.r = last_at_most(pre, a.R, div(b0, a.by_heads));
   at.nc = ncand[at.r];
   {
     const int nb = (at.nc + PER - 1) / PER;
-    const int64_t in = b0 - int64_t(pre[at.r]) * a.heads;
-    at.h = static_cast<int>(in / nb);
-    at.c0 = static_cast<int>(in - int64_t(at.h) * nb) * PER;
+    const int in = b0 - pre[at.r] * a.heads;
+    at.h = in / nb;
+    at.c0 = (in - at.h * nb) * PER;
   }
   const auto advance = [&](Pos p) {  // (called while a batch is left: a request with candidates is)
     p.c0 += PER;
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
   };
   const auto page_of = [&](const Pos& p) {  // lane i: page of candidate c0 + i, or -1
     if (lane >= PER || p.c0 + lane >= p.nc) return -1;
-    const int page = a.table[int64_t(p.r) * a.max_pages + first + p.c0 + lane];
+    const int page = a.table[int64_t(p.r) * a.max_pages + a.first + p.c0 + lane];
     if (page >= 0 && page < a.n_pages) return page;
     report(a.status, RBA_ERR_BOUNDS, kWherePaged, page);
     return -1;
@@ -130,8 +132,8 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
   Pos ahead = at;
   int page = page_of(at);
   unsigned rows[kRingPlaces];  // lanes whose candidate's row is in the place
-  const auto issue = [&](int n) {  // the warp's n-th batch (b0 + n) into place n % kRingPlaces
-    if (b0 + n >= b1) return;
+  const auto issue = [&](int n) {  // the warp's n-th batch into place n % kRingPlaces
+    if (n >= batches) return;
     const int i = n % kRingPlaces;
     const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
 #pragma unroll
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
       if (j == i) rows[j] = there;
     arm_and_copy(bar0 + i * 8, lane == 0, ROW * __popc(there), ring0 + i * PLACE,
                  a.rep + (int64_t(page) * a.heads + ahead.h) * P, page >= 0 ? ROW : 0);
-    if (b0 + n + 1 < b1) {
+    if (n + 1 < batches) {
       ahead = advance(ahead);
       page = page_of(ahead);
     }
@@ -147,7 +149,6 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
 #pragma unroll
   for (int n = 0; n < kRingPlaces; ++n) issue(n);
   load_q(at);
-  const int batches = static_cast<int>(b1 - b0);
   for (int n = 0; n < batches; ++n) {
     const int i = n % kRingPlaces;
     if (!await_phase(bar0 + i * 8, (n / kRingPlaces) & 1)) {
@@ -222,7 +223,9 @@ extern "C" rba_status rba_paged_select(const rba_paged* s, const void* q,
   if (k == 0) return RBA_OK;
   if (q == nullptr || idx == nullptr || workspace == nullptr) return RBA_ERR_INVALID_ARG;
   const int row = most_candidates(s, sink, window);
-  if (row > kPagedMaxCandidates || int64_t(n_requests) * s->d.n_kv_heads > INT32_MAX)
+  // (batches of scores are counted in 31 bits)
+  if (row > kPagedMaxCandidates ||
+      int64_t(n_requests) * s->d.n_kv_heads * (row / kBatch + 1) > INT32_MAX)
     return RBA_ERR_UNSUPPORTED;
   if (ws_bytes < size_t(n_requests) * s->d.n_kv_heads * row * sizeof(float))
     return RBA_ERR_WORKSPACE;
@@ -245,6 +248,11 @@ extern "C" rba_status rba_paged_select(const rba_paged* s, const void* q,
   a.sink = sink;
   a.window = window;
   a.row = row;
+  a.first = sink / a.bs;
+  a.by_bs = fast_div(a.bs);
+  a.by_heads = fast_div(a.heads);
+  const int grid = num_sms() * kScoreCtas;
+  a.by_warps = fast_div(grid * (kScoreThreads / 32));
   a.q_vec = reinterpret_cast<uintptr_t>(q) % (4 * dtype_size(s->d.dtype)) == 0 &&
             ((q_request_stride | q_head_stride) & 3) == 0;
   if (row > 0) {
@@ -256,8 +264,8 @@ extern "C" rba_status rba_paged_select(const rba_paged* s, const void* q,
                                : paged_score_kernel<__nv_bfloat16, 64>)
             : (s->pitch == 128 ? paged_score_kernel<float, 128> : paged_score_kernel<float, 64>);
     RBA_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kernel), smem));
-    RBA_CUDA_TRY(launch_dependent(kernel, static_cast<unsigned>(num_sms() * kScoreCtas),
-                                  kScoreThreads, smem, stream, a));
+    RBA_CUDA_TRY(launch_dependent(kernel, static_cast<unsigned>(grid), kScoreThreads, smem, stream,
+                                  a));
   }
   return launch_topk_paged(a.scores, row, n_requests * s->d.n_kv_heads, s->d.n_kv_heads, a.lens,
                            a.bs, a.max_pages, sink, window, k, idx, stream);

@@ -276,8 +276,9 @@ __global__ void __launch_bounds__(kRowThreads) topk_rows_kernel(const float* __r
 // The same for the rows of a paged memory, each as long as its request has candidates; a row
 // with fewer than k of them is filled up with -1.
 __global__ void __launch_bounds__(kRowThreads) topk_paged_rows_kernel(
-    const float* __restrict__ scores, int row_stride, int heads, const int32_t* __restrict__ lens,
-    int bs, int max_pages, int sink, int window, int k, int32_t* __restrict__ idx) {
+    const float* __restrict__ scores, int row_stride, FastDiv by_heads,
+    const int32_t* __restrict__ lens, FastDiv by_bs, int max_pages, int first, int sink, int window,
+    int k, int32_t* __restrict__ idx) {
   wait_for_stream();
   extern __shared__ __align__(16) char sm[];
   float* vals = reinterpret_cast<float*>(sm);                               // [row_stride]
@@ -288,9 +289,9 @@ __global__ void __launch_bounds__(kRowThreads) topk_paged_rows_kernel(
   __shared__ int s_misc[8];
   __shared__ float s_f[2 * kRowWarps];
   const int64_t row = blockIdx.x;
-  const int len = lens[row / heads];
-  const PagedGeo g =
-      paged_geo(len < 0 || len > int64_t(max_pages) * bs ? 0 : len, bs, sink, window);
+  const int len = lens[div(blockIdx.x, by_heads)];
+  const PagedGeo g = paged_geo(len < 0 || len > int64_t(max_pages) * by_bs.d ? 0 : len, by_bs,
+                               first, sink, window);
   const int n = min(g.nc, row_stride);
   const float* s = scores + row * row_stride;
   int32_t* dst = idx + row * k;
@@ -305,22 +306,23 @@ __global__ void __launch_bounds__(kRowThreads) topk_paged_rows_kernel(
 
 // The same by one warp per row, for rows of up to 1024 candidates and k up to 16: the keys stay in
 // registers, and each of k rounds takes the warp's largest key, the lowest position first.  A round
-// costs about 100 instructions of one warp; a CTA's radix select costs its dozen barriers whatever k
-// is.  512 rows of up to 650 scores, k = 4: 6.3 us against 9.5 for the CTA a row; from k = 32 on the
-// CTA is the faster one.
+// costs about 100 instructions of one warp; a CTA's radix select costs its dozen barriers whatever
+// k is.  512 rows of up to 650 scores, k = 4: 6.3 us against 9.5 for the CTA a row; from k = 32 on
+// the CTA is the faster one.
 constexpr int kWarpRowN = 1024, kWarpRowK = 16, kWarpRowThreads = 128;
 __global__ void __launch_bounds__(kWarpRowThreads) topk_paged_warp_kernel(
-    const float* __restrict__ scores, int row_stride, int rows, int heads,
-    const int32_t* __restrict__ lens, int bs, int max_pages, int sink, int window, int k,
-    int32_t* __restrict__ idx) {
+    const float* __restrict__ scores, int row_stride, int rows, FastDiv by_heads,
+    const int32_t* __restrict__ lens, FastDiv by_bs, int max_pages, int first, int sink, int window,
+    int k, int32_t* __restrict__ idx) {
   wait_for_stream();
   constexpr int kPerLane = kWarpRowN / 32;
   const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int len = lens[row / heads];
-  const PagedGeo g =
-      paged_geo(len < 0 || len > int64_t(max_pages) * bs ? 0 : len, bs, sink, window);
+  const int at_row = blockIdx.x * (kWarpRowThreads / 32) + (threadIdx.x >> 5);
+  if (at_row >= rows) return;
+  const int64_t row = at_row;
+  const int len = lens[div(at_row, by_heads)];
+  const PagedGeo g = paged_geo(len < 0 || len > int64_t(max_pages) * by_bs.d ? 0 : len, by_bs,
+                               first, sink, window);
   const int n = min(g.nc, row_stride);
   const float* s = scores + row * row_stride;
   uint32_t key[kPerLane];  // 0: none (no score's key is 0)
@@ -365,19 +367,20 @@ __global__ void __launch_bounds__(kWarpRowThreads) topk_paged_warp_kernel(
 rba_status launch_topk_paged(const float* scores, int row_stride, int rows, int heads,
                              const int32_t* lens, int bs, int max_pages, int sink, int window,
                              int k, int32_t* idx, cudaStream_t stream) {
+  const FastDiv by_heads = fast_div(heads), by_bs = fast_div(bs);
   if (row_stride <= kWarpRowN && k <= kWarpRowK) {
     constexpr int kRows = kWarpRowThreads / 32;
     RBA_CUDA_TRY(launch_dependent(topk_paged_warp_kernel,
                                   static_cast<unsigned>((rows + kRows - 1) / kRows),
-                                  kWarpRowThreads, 0, stream, scores, row_stride, rows, heads, lens,
-                                  bs, max_pages, sink, window, k, idx));
+                                  kWarpRowThreads, 0, stream, scores, row_stride, rows, by_heads,
+                                  lens, by_bs, max_pages, sink / bs, sink, window, k, idx));
     return RBA_OK;
   }
   const size_t smem = size_t(row_stride) * 5 + 16;
   RBA_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(topk_paged_rows_kernel), smem));
   RBA_CUDA_TRY(launch_dependent(topk_paged_rows_kernel, static_cast<unsigned>(rows), kRowThreads,
-                                smem, stream, scores, row_stride, heads, lens, bs, max_pages, sink,
-                                window, k, idx));
+                                smem, stream, scores, row_stride, by_heads, lens, by_bs, max_pages,
+                                sink / bs, sink, window, k, idx));
   return RBA_OK;
 }
 
