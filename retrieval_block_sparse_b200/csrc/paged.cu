@@ -84,6 +84,8 @@ __device__ __forceinline__ bool last_cta(int32_t* count, int* s_last) {
 // the table that this call writes, so the CTAs need no order among them, and the one that
 // finishes last moves the lengths and the free count.  A call that cannot be served whole
 // (too few pages, a table row too short, a bad count) changes nothing.
+// Bound by latency, the chain lengths, scan, slots, lengths: with a truncate after it, 256 requests
+// that grow by a token take 9.0 us, 33 that grow by 96K tokens in 24-token pages 12.3.
 __global__ void __launch_bounds__(kTableThreads) extend_kernel(TableArgs a) {
   __shared__ int32_t s_start[kMaxRequests + 1], s_page[kMaxRequests + 1];
   __shared__ int64_t s_w[2][32];
