@@ -580,7 +580,7 @@ rba_status rba_paged_read(const rba_paged* store, const int32_t* slots, int32_t 
  *   workspace >= rba_paged_select_workspace_size() (no contents are kept in it)
  * Which pages a row of scores with a NaN among them selects is not specified (they are candidates
  * all the same); other rows are not affected.  Errors: INVALID_ARG, UNSUPPORTED (more than 16384
- * candidates in max_pages, or more than 2^31 - 1 rows), WORKSPACE, CUDA. */
+ * candidates in max_pages, or 2^31 scores in all, eight to a row at least), WORKSPACE, CUDA. */
 rba_status rba_paged_select(const rba_paged* store, const void* q, int64_t q_request_stride,
                             int64_t q_head_stride, int32_t n_requests, int32_t k, int32_t sink,
                             int32_t window, int32_t* idx, void* workspace, size_t ws_bytes,
@@ -598,7 +598,7 @@ size_t rba_paged_select_workspace_size(const rba_paged* store);
  *   out  device fp32 [n_requests][Hq][D];  lse device fp32 [n_requests][Hq] or NULL
  *   workspace >= rba_paged_attend_workspace_size(), 16-byte aligned (no contents are kept in it)
  * Errors: INVALID_ARG, UNSUPPORTED (n_requests * Hkv * ceil(group / 8) units of up to
- * ceil((max_pages + 2) * strips of a page / 2) + 8 each are more than 2^31 - 1 in all, or more than
+ * ceil((max_pages + 2) * strips of a page / 2) + 10 each are more than 2^31 - 1 in all, or more than
  * 2^31 - 1 rows of q), WORKSPACE, CUDA. */
 rba_status rba_paged_attend(const rba_paged* store, const void* q, int64_t q_request_stride,
                             int64_t q_head_stride, int32_t n_requests, const int32_t* idx,

@@ -695,10 +695,29 @@ class PagedStore:
         k_new, v_new [n][Hkv][D] (n may be larger: rows past them are ignored), then q [R][Hq][D]
         attends to sink, its k best pages and window.  Returns (idx, out, lse).  With every
         buffer given it can be captured once and replayed."""
-        n, R = k_new.shape[0], n_new.shape[0]  # (a call that is refused leaves the store as it was)
+        # everything is checked before the first call: a refused step leaves the store as it was
+        n, R, i32, f32 = k_new.shape[0], n_new.shape[0], torch.int32, torch.float32
+        if min(k, sink, window) < 0:
+            raise ValueError(f"k, sink, window: expected 0 or more, got {k}, {sink}, {window}")
         self._rows("k_new", k_new, n, self.Hkv)
         self._rows("v_new", v_new, n, self.Hkv)
         self._rows("q", q, R, self.Hq)
+        for name, t, shape, dt in (("n_new", n_new, (R,), i32), ("slots", slots, (n,), i32),
+                                   ("starts", starts, (R + 1,), i32),
+                                   ("idx", idx, (R, self.Hkv, k), i32),
+                                   ("out", out, (R, self.Hq, self.D), f32),
+                                   ("lse", lse, (R, self.Hq), f32)):
+            if t is not None:
+                self._arg(name, t, shape, dt)
+        if select_workspace is None and k:
+            select_workspace = self.select_workspace()
+        if workspace is None:
+            workspace = self.attend_workspace()
+        with torch.cuda.device(self.device):
+            if (k and self._bytes(select_workspace)[1]
+                    < _LIB.rba_paged_select_workspace_size(self.handle)) or \
+                    self._bytes(workspace)[1] < _LIB.rba_paged_attend_workspace_size(self.handle):
+                raise RbaError(ERR_WORKSPACE, "decode_step")
         slots, _ = self.extend(n_new, k_new.shape[0], slots=slots, starts=starts)
         self.append(slots, k_new, v_new)
         idx = self.select(q, k, sink, window, idx=idx, workspace=select_workspace) if k else None

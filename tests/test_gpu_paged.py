@@ -640,6 +640,19 @@ def test_decode_step_is_the_four_calls(rba):
                 (qd, k, v, new.long())):
         with pytest.raises(ValueError):
             a.st.decode_step(*bad, 2, 4, 9)
+    f32 = dict(dtype=torch.float32, device="cuda")
+    for bad in (dict(idx=i32([[0]])), dict(out=torch.empty((3, 4, 32), **f32)),
+                dict(lse=torch.empty((4, 3), **f32)), dict(slots=i32([0])),
+                dict(starts=i32([0])), dict(workspace=torch.empty(64, **f32))):
+        with pytest.raises(ValueError):
+            a.st.decode_step(qd, k, v, new, 2, 4, 9, **bad)
+    tiny = torch.empty(16, dtype=torch.uint8, device="cuda")
+    for bad in (dict(select_workspace=tiny), dict(workspace=tiny)):
+        with pytest.raises(rba.RbaError):
+            a.st.decode_step(qd, k, v, new, 2, 4, 9, **bad)
+    for bad in ((-1, 4, 9), (2, -1, 9), (2, 4, -1)):
+        with pytest.raises(ValueError):
+            a.st.decode_step(qd, k, v, new, *bad)
     assert a.st.lens.tolist() == [41, 3, 17]  # a refused step grows nothing
     a.st.check()
 
