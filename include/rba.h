@@ -580,7 +580,8 @@ rba_status rba_paged_read(const rba_paged* store, const int32_t* slots, int32_t 
  *   workspace >= rba_paged_select_workspace_size() (no contents are kept in it)
  * Which pages a row of scores with a NaN among them selects is not specified (they are candidates
  * all the same); other rows are not affected.  Errors: INVALID_ARG, UNSUPPORTED (more than 16384
- * candidates in max_pages, or 2^31 scores in all, eight to a row at least), WORKSPACE, CUDA. */
+ * candidates c in max_pages, or n_requests * Hkv * (c / 8 + 1) more than 2^31 - 1), WORKSPACE,
+ * CUDA. */
 rba_status rba_paged_select(const rba_paged* store, const void* q, int64_t q_request_stride,
                             int64_t q_head_stride, int32_t n_requests, int32_t k, int32_t sink,
                             int32_t window, int32_t* idx, void* workspace, size_t ws_bytes,
