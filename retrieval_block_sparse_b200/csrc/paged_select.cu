@@ -12,9 +12,9 @@ namespace rba {
 namespace {
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreCtas = 2;  // per SM
+constexpr int kScoreCtas = 3;  // per SM
 constexpr int kBatch = 8;      // candidate rows that a lane has a share of at a time
-constexpr int kRingPlaces = 3; // batches in a warp's ring: 4 KB each
+constexpr int kRingPlaces = 2; // batches in a warp's ring: 4 KB each
 
 struct SelectArgs {
   const void* q;
@@ -53,13 +53,14 @@ __device__ int scan_batches(const SelectArgs& a, int per, int32_t* pre, int32_t*
 }
 
 // A warp takes a run of batches of PER candidates, through its own ring of bulk copies (a row is
-// one run of bytes): 4 KB a batch, three batches on their way, whatever the warp is computing.
+// one run of bytes): 4 KB a batch, two batches on their way, whatever the warp is computing.
 // The page numbers of the batch to be copied next are loaded one copy ahead.  The sums are added
 // over lanes by halving exchanges (each step halves the rows a lane carries): two or three per row
-// instead of five.  86 MB of page means and the choice among them take 28.1 us, the means alone
-// about 20 (4.3 TB/s); with rows loaded into registers a batch ahead, 16 warps an SM left the memory
-// idle half the time (26 us for the means).  What is left is the scan of the requests before the
-// first copy (about 4 us) and the latency and issue slots of the 64-bit sums.
+// instead of five.  86 MB of page means and the choice among them take 27.4 us (28.2 with two CTAs
+// an SM of three batches a warp), the means alone about 19 (4.5 TB/s); with rows loaded into
+// registers a batch ahead, 16 warps an SM left the memory idle half the time (26 us for the means).
+// What is left is the scan of the requests before the first copy (about 4 us) and the latency and
+// issue slots of the 64-bit sums.
 template <typename T, int P>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(SelectArgs a) {
   constexpr int LPR = P / 4, RPW = 32 / LPR;  // lanes a row, rows a warp reads at once
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) paged_score_kernel(
   const int one = scan_batches(a, PER, pre, ncand, s_w);
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   // the warp's share of all batches (warps of one CTA lie far apart, so that few batches use every
-  // SM).  With 64-bit and plain divisions here a selection over 86 MB took 30.1 us, not 28.1.
+  // SM).  With 64-bit and plain divisions here a selection over 86 MB took 2 us more.
   const int all = one * a.heads, w = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
   const int share = div(all, a.by_warps), more = all - share * static_cast<int>(a.by_warps.d);
   const int b0 = w * share + min(w, more), batches = share + (w < more);
