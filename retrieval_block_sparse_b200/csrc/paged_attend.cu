@@ -34,9 +34,9 @@
 // fence and a merge by the last worker to arrive, which few warps would then wait for.  Where no
 // unit can be longer than kWholePairs, workers take whole units and there is no second kernel.
 //
-// Measured, with the merge: 4 requests of 128K tokens, 8 x 4 heads, bf16: 122.9 us, 4.9 TB/s of codes
-// and scales, 74 % of a plain copy's rate; 64 requests to 8K tokens, 4 x 8 heads, 32-bit: 59 us,
-// 2.4 TB/s.  Both are bound by the issue of 331 and about 470 instructions a strip.  8192 attended
+// Measured, with the merge: 4 requests of 128K tokens, 8 x 4 heads, bf16: 122.9 us, 4.9 TB/s of
+// codes and scales, 74 % of a plain copy's rate; 64 requests to 8K tokens, 4 x 8 heads, 32-bit:
+// 59 us, 2.4 TB/s.  Both are bound by the issue of 331 and about 470 instructions a strip.  8192 attended
 // tokens of one request: 12.5 us, bound by the chain launch, scan, table, copy, merge.
 #include <cuda_fp16.h>
 
