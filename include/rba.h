@@ -577,7 +577,7 @@ rba_status rba_paged_read(const rba_paged* store, const int32_t* slots, int32_t 
  *   q    device dtype, rows (r, head) as above, r < n_requests
  *   idx  device int32 [n_requests][Hkv][k], written: pages of the request (columns of its table
  *        row) ascending; -1 past its candidates
- *   workspace >= rba_paged_select_workspace_size() (no contents are kept in it)
+ *   workspace >= rba_paged_select_workspace_size(), 4-byte aligned (no contents are kept in it)
  * Which pages a row of scores with a NaN among them selects is not specified (they are candidates
  * all the same); other rows are not affected.  Errors: INVALID_ARG, UNSUPPORTED (more than 16384
  * candidates c in max_pages, or n_requests * Hkv * (c / 8 + 1) more than 2^31 - 1), WORKSPACE,

@@ -223,6 +223,7 @@ extern "C" rba_status rba_paged_select(const rba_paged* s, const void* q,
     return RBA_ERR_INVALID_ARG;
   if (k == 0) return RBA_OK;
   if (q == nullptr || idx == nullptr || workspace == nullptr) return RBA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) % alignof(float) != 0) return RBA_ERR_INVALID_ARG;
   const int row = most_candidates(s, sink, window);
   // (batches of scores are counted in 31 bits)
   if (row > kPagedMaxCandidates ||

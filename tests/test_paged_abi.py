@@ -106,6 +106,12 @@ def test_select_refuses(L, store):
     L.rba_paged_destroy(h)
 
 
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_select_wants_a_workspace_of_floats(L, store, off):
+    assert L.rba_paged_select(store, FAKE, 1024, 128, 4, 3, 0, 0, FAKE, FAKE + off, 1 << 20,
+                              None) == INVALID
+
+
 def test_attend_refuses(L, store):
     def att(s=store, q=FAKE, n=4, idx=FAKE, k=3, sink=0, window=0, out=FAKE, ws=FAKE, nb=1 << 30):
         return L.rba_paged_attend(s, q, 1024, 128, n, idx, k, sink, window, F(0.1), out, None, ws,
