@@ -607,6 +607,15 @@ rba_status rba_paged_attend(const rba_paged* store, const void* q, int64_t q_req
                             float* lse, void* workspace, size_t ws_bytes, cudaStream_t stream);
 size_t rba_paged_attend_workspace_size(const rba_paged* store);
 
+/* Host only, launches nothing: the error that rba_paged_append (n_rows rows), rba_paged_select or
+ * rba_paged_attend would return for these sizes, numbers and workspaces, RBA_OK where none would.
+ * For a step that has to be refused before rba_paged_extend has changed the store.
+ * select_workspace may be NULL when k = 0. */
+rba_status rba_paged_step_check(const rba_paged* store, int32_t n_requests, int32_t n_rows,
+                                int32_t k, int32_t sink, int32_t window,
+                                const void* select_workspace, size_t select_ws_bytes,
+                                const void* attend_workspace, size_t attend_ws_bytes);
+
 /* As rba_store_check: synchronises `stream`, returns the first device-side error since the last
  * check and clears it. */
 rba_status rba_paged_check(const rba_paged* store, cudaStream_t stream);

@@ -187,6 +187,14 @@ cudaError_t launch_dependent(void (*kernel)(A...), unsigned grid, int threads, s
   return e;
 }
 
+// The host-side refusals of the calls of a decode step (RBA_OK: none): the library's limits, and
+// the workspaces'.  Each call makes its own check; rba_paged_step_check makes all of them.
+rba_status refuse_append(const rba_paged* s, int32_t n);
+rba_status refuse_select(const rba_paged* s, int32_t n_requests, int32_t k, int32_t sink,
+                         int32_t window, const void* workspace, size_t ws_bytes);
+rba_status refuse_attend(const rba_paged* s, int32_t n_requests, int32_t k, int32_t sink,
+                         int32_t window, const void* workspace, size_t ws_bytes);
+
 // Top k per row of scores [rows][row_stride], row = request * heads + kv head: the request's
 // candidates only, written as page numbers ascending, then -1.
 rba_status launch_topk_paged(const float* scores, int row_stride, int rows, int heads,

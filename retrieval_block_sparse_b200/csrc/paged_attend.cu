@@ -1030,25 +1030,11 @@ rba_status launch(const PagedAttendArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
-}  // namespace rba
 
-extern "C" size_t rba_paged_attend_workspace_size(const rba_paged* s) {
-  using namespace rba;
-  if (s == nullptr) return 0;
-  return unit_bytes(s) + size_t(num_sms()) * kCtasPerSm * kWarps * 2 *
-                               (wide_of(s) ? 8 : 4) * (s->pitch + 4) * sizeof(float);
-}
-
-extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
-                                       int64_t q_request_stride, int64_t q_head_stride,
-                                       int32_t n_requests, const int32_t* idx, int32_t k,
-                                       int32_t sink, int32_t window, float scale, float* out,
-                                       float* lse, void* workspace, size_t ws_bytes,
-                                       cudaStream_t stream) {
-  using namespace rba;
-  if (s == nullptr || q == nullptr || out == nullptr || workspace == nullptr || n_requests <= 0 ||
-      n_requests > s->d.max_requests || k < 0 || (k > 0 && idx == nullptr) || sink < 0 ||
-      window < 0)
+rba_status refuse_attend(const rba_paged* s, int32_t n_requests, int32_t k, int32_t sink,
+                         int32_t window, const void* workspace, size_t ws_bytes) {
+  if (s == nullptr || workspace == nullptr || n_requests <= 0 ||
+      n_requests > s->d.max_requests || k < 0 || sink < 0 || window < 0)
     return RBA_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return RBA_ERR_INVALID_ARG;
   if (ws_bytes < rba_paged_attend_workspace_size(s)) return RBA_ERR_WORKSPACE;
@@ -1059,6 +1045,41 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
   if (unit > INT32_MAX || unit * units > INT32_MAX ||
       int64_t(n_requests) * s->d.n_q_heads > INT32_MAX)
     return RBA_ERR_UNSUPPORTED;
+  return RBA_OK;
+}
+
+}  // namespace rba
+
+extern "C" size_t rba_paged_attend_workspace_size(const rba_paged* s) {
+  using namespace rba;
+  if (s == nullptr) return 0;
+  return unit_bytes(s) + size_t(num_sms()) * kCtasPerSm * kWarps * 2 *
+                               (wide_of(s) ? 8 : 4) * (s->pitch + 4) * sizeof(float);
+}
+
+extern "C" rba_status rba_paged_step_check(const rba_paged* s, int32_t n_requests, int32_t n_rows,
+                                           int32_t k, int32_t sink, int32_t window,
+                                           const void* select_workspace, size_t select_bytes,
+                                           const void* attend_workspace, size_t attend_bytes) {
+  using namespace rba;
+  rba_status r = refuse_append(s, n_rows);
+  if (r == RBA_OK)
+    r = refuse_select(s, n_requests, k, sink, window, select_workspace, select_bytes);
+  if (r == RBA_OK)
+    r = refuse_attend(s, n_requests, k, sink, window, attend_workspace, attend_bytes);
+  return r;
+}
+
+extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
+                                       int64_t q_request_stride, int64_t q_head_stride,
+                                       int32_t n_requests, const int32_t* idx, int32_t k,
+                                       int32_t sink, int32_t window, float scale, float* out,
+                                       float* lse, void* workspace, size_t ws_bytes,
+                                       cudaStream_t stream) {
+  using namespace rba;
+  if (q == nullptr || out == nullptr || (k > 0 && idx == nullptr)) return RBA_ERR_INVALID_ARG;
+  const rba_status refused = refuse_attend(s, n_requests, k, sink, window, workspace, ws_bytes);
+  if (refused != RBA_OK) return refused;
   PagedAttendArgs a = {};
   a.q = q;
   a.q_req = q_request_stride;

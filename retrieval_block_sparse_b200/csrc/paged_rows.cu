@@ -428,6 +428,14 @@ unsigned run_grid(const RowArgs& a, int slots) {
 }
 
 }  // namespace
+
+rba_status refuse_append(const rba_paged* s, int32_t n) {
+  if (s == nullptr || n < 0) return RBA_ERR_INVALID_ARG;
+  if (n == 0) return RBA_OK;
+  const RowArgs a = row_args(s, nullptr, n);
+  return run_grid(a, a.window) == 0 ? RBA_ERR_UNSUPPORTED : RBA_OK;
+}
+
 }  // namespace rba
 
 extern "C" rba_status rba_paged_append(rba_paged* s, const int32_t* slots, int32_t n,
@@ -439,6 +447,8 @@ extern "C" rba_status rba_paged_append(rba_paged* s, const int32_t* slots, int32
   if (s == nullptr || n < 0) return RBA_ERR_INVALID_ARG;
   if (n == 0) return RBA_OK;
   if (slots == nullptr || k == nullptr || v == nullptr) return RBA_ERR_INVALID_ARG;
+  const rba_status refused = refuse_append(s, n);
+  if (refused != RBA_OK) return refused;
   RowArgs a = row_args(s, slots, n);
   a.k = k;
   a.v = v;
@@ -451,7 +461,6 @@ extern "C" rba_status rba_paged_append(rba_paged* s, const int32_t* slots, int32
   a.vec = (reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % unit == 0 &&
           ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 3) == 0;
   const unsigned grid = run_grid(a, a.window);
-  if (grid == 0) return RBA_ERR_UNSUPPORTED;
   // means: 128 slots a CTA, fewer where that would leave SMs without two (8192 tokens of 8 heads:
   // 24.9 us with their read-back, 25.8 with 64 slots; 777 of 32 heads: 20.2 and 18.8)
   int words = kMeanWords, log_warps = 0;  // (log_warps: of a page's warps)

@@ -205,6 +205,25 @@ int most_candidates(const rba_paged* s, int sink, int window) {
 }
 
 }  // namespace
+
+rba_status refuse_select(const rba_paged* s, int32_t n_requests, int32_t k, int32_t sink,
+                         int32_t window, const void* workspace, size_t ws_bytes) {
+  if (s == nullptr || n_requests <= 0 || n_requests > s->d.max_requests || k < 0 || sink < 0 ||
+      window < 0)
+    return RBA_ERR_INVALID_ARG;
+  if (k == 0) return RBA_OK;
+  if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % alignof(float) != 0)
+    return RBA_ERR_INVALID_ARG;
+  const int row = most_candidates(s, sink, window);
+  // (batches of scores are counted in 31 bits)
+  if (row > kPagedMaxCandidates ||
+      int64_t(n_requests) * s->d.n_kv_heads * (row / kBatch + 1) > INT32_MAX)
+    return RBA_ERR_UNSUPPORTED;
+  if (ws_bytes < size_t(n_requests) * s->d.n_kv_heads * row * sizeof(float))
+    return RBA_ERR_WORKSPACE;
+  return RBA_OK;
+}
+
 }  // namespace rba
 
 extern "C" size_t rba_paged_select_workspace_size(const rba_paged* s) {
@@ -218,19 +237,10 @@ extern "C" rba_status rba_paged_select(const rba_paged* s, const void* q,
                                        int32_t window, int32_t* idx, void* workspace,
                                        size_t ws_bytes, cudaStream_t stream) {
   using namespace rba;
-  if (s == nullptr || n_requests <= 0 || n_requests > s->d.max_requests || k < 0 || sink < 0 ||
-      window < 0)
-    return RBA_ERR_INVALID_ARG;
-  if (k == 0) return RBA_OK;
-  if (q == nullptr || idx == nullptr || workspace == nullptr) return RBA_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(workspace) % alignof(float) != 0) return RBA_ERR_INVALID_ARG;
+  if (k > 0 && (q == nullptr || idx == nullptr)) return RBA_ERR_INVALID_ARG;
+  const rba_status refused = refuse_select(s, n_requests, k, sink, window, workspace, ws_bytes);
+  if (refused != RBA_OK || k == 0) return refused;
   const int row = most_candidates(s, sink, window);
-  // (batches of scores are counted in 31 bits)
-  if (row > kPagedMaxCandidates ||
-      int64_t(n_requests) * s->d.n_kv_heads * (row / kBatch + 1) > INT32_MAX)
-    return RBA_ERR_UNSUPPORTED;
-  if (ws_bytes < size_t(n_requests) * s->d.n_kv_heads * row * sizeof(float))
-    return RBA_ERR_WORKSPACE;
   SelectArgs a = {};
   a.q = q;
   a.q_req = q_request_stride;

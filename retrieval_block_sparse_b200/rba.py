@@ -80,6 +80,8 @@ SIGNATURES = {
     "rba_paged_attend": (_c_i32, [_p, _p, _c_i64, _c_i64, _c_i32, _p, _c_i32, _c_i32, _c_i32,
                                   _c_f32, _p, _p, _p, _c_size, _p]),
     "rba_paged_attend_workspace_size": (_c_size, [_p]),
+    "rba_paged_step_check": (_c_i32, [_p, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _p, _c_size, _p,
+                                      _c_size]),
     "rba_paged_check": (_c_i32, [_p, _p]),
     "rba_store_check": (_c_i32, [_p, _p]),
     "rba_row_pitch": (_c_i32, [_c_i32]),
@@ -713,11 +715,10 @@ class PagedStore:
             select_workspace = self.select_workspace()
         if workspace is None:
             workspace = self.attend_workspace()
-        with torch.cuda.device(self.device):
-            if (k and self._bytes(select_workspace)[1]
-                    < _LIB.rba_paged_select_workspace_size(self.handle)) or \
-                    self._bytes(workspace)[1] < _LIB.rba_paged_attend_workspace_size(self.handle):
-                raise RbaError(ERR_WORKSPACE, "decode_step")
+        spaces = (*(self._bytes(select_workspace) if k else (None, 0)), *self._bytes(workspace))
+        with torch.cuda.device(self.device):  # (the library's own limits)
+            _check(_LIB.rba_paged_step_check(self.handle, R, n, k, sink, window, *spaces),
+                   "decode_step")
         slots, _ = self.extend(n_new, k_new.shape[0], slots=slots, starts=starts)
         self.append(slots, k_new, v_new)
         idx = self.select(q, k, sink, window, idx=idx, workspace=select_workspace) if k else None

@@ -657,6 +657,33 @@ def test_decode_step_is_the_four_calls(rba):
     a.st.check()
 
 
+@pytest.mark.parametrize("shape,k,status", [
+    (dict(heads=1, page=16, columns=20000), 3, 2),             # more candidates than select takes
+    (dict(heads=256, page=16, columns=2 ** 20, requests=16), 0, 2)])  # a line attend cannot count
+def test_a_step_that_the_library_refuses_grows_nothing(rba, shape, k, status):
+    p = Pair(rba, 59, group=1, dim=64, n_pages=4, **shape)
+    R = len(p.m.lens)
+    q, x = p.queries()[1], torch.ones((1, p.heads, 64), device="cuda").bfloat16()
+    new = i32([1] + [0] * (R - 1))
+    before = [t.clone() for t in (p.st.lens, p.st.n_free, p.st.pool)]
+    with pytest.raises(rba.RbaError) as e:
+        p.st.decode_step(q, x, x, new, k, 0, 0)
+    assert e.value.status == status
+    assert all(torch.equal(a, b) for a, b in zip(before, (p.st.lens, p.st.n_free, p.st.pool)))
+    p.st.check()
+
+
+def test_a_step_with_a_workspace_off_its_boundary_grows_nothing(rba):
+    p = Pair(rba, 61)
+    q, x = p.queries()[1], torch.ones((1, 2, 128), device="cuda").bfloat16()
+    wide = torch.empty(p.st.attend_workspace().numel() + 16, dtype=torch.uint8, device="cuda")
+    for bad in (dict(workspace=wide[4:]), dict(select_workspace=wide[2:])):
+        with pytest.raises(rba.RbaError) as e:
+            p.st.decode_step(q, x, x, i32([1, 0, 0]), 2, 0, 0, **bad)
+        assert e.value.status == rba.ERR_INVALID_ARG
+        assert p.st.lens.tolist() == [0, 0, 0]
+
+
 def test_keys_that_are_not_finite_leave_other_rows_alone(rba):
     """A page mean that is not a number makes its own row's choice unspecified, no other's."""
     for k, columns in ((3, 24), (17, 80)):  # a warp's rows, a CTA's

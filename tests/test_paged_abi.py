@@ -125,5 +125,31 @@ def test_attend_refuses(L, store):
     L.rba_paged_destroy(h)
 
 
+def test_step_check_refuses_what_a_steps_calls_would(L, store):
+    ws = L.rba_paged_attend_workspace_size(store)
+
+    def chk(s=store, n=4, rows=4, k=3, sink=0, window=0, sel=FAKE, nsel=1 << 20, att=FAKE,
+            natt=1 << 30):
+        return L.rba_paged_step_check(s, n, rows, k, sink, window, sel, nsel, att, natt)
+    assert chk() == chk(rows=0) == chk(k=0, sel=None, nsel=0) == 0
+    assert chk(nsel=4 * 2 * 16 * 4, natt=ws) == 0
+    assert chk(s=None) == chk(n=0) == chk(n=5) == chk(rows=-1) == chk(k=-1) == chk(sink=-1) == \
+        chk(window=-1) == chk(sel=None) == chk(sel=FAKE + 2) == chk(att=None) == \
+        chk(att=FAKE + 4) == INVALID
+    assert chk(nsel=4 * 2 * 16 * 4 - 1) == chk(natt=ws - 1) == WORKSPACE
+    s, h = _create(L, max_pages=20000)
+    assert s == 0 and chk(s=h) == UNSUPPORTED
+    assert chk(s=h, window=20000 * 32 - 100) == chk(s=h, k=0) == 0  # 4 candidates, none
+    L.rba_paged_destroy(h)
+    s, h = _create(L, page_size=1, max_pages=1 << 30, max_requests=2)
+    assert s == 0 and chk(s=h, n=2, k=0, natt=1 << 62) == UNSUPPORTED
+    L.rba_paged_destroy(h)
+    s, h = _create(L, n_q_heads=64, n_kv_heads=64)
+    big = (1 << 31) - 1
+    assert s == 0 and chk(s=h, rows=big) == UNSUPPORTED == L.rba_paged_append(
+        h, FAKE, big, FAKE, 8192, 128, FAKE, 8192, 128, None)
+    L.rba_paged_destroy(h)
+
+
 def test_check_wants_a_store(L):
     assert L.rba_paged_check(None, None) == INVALID
