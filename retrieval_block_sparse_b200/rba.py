@@ -490,6 +490,16 @@ class _PagedBuffers(ctypes.Structure):
                                   "status")]
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _fits(**numbers):
+    """Refuses numbers that the library would take for others (ctypes cuts them to 32 bits)."""
+    for name, x in numbers.items():
+        if not -_MOST - 1 <= x <= _MOST:
+            raise ValueError(f"{name}: expected a 32-bit number, got {x}")
+
+
 class PagedStore:
     """A paged memory in 4 bits for requests of different lengths (rba_paged_* in rba.h).
 
@@ -509,6 +519,8 @@ class PagedStore:
                  lens=None, free=None, n_free=None):
         if dtype not in ("bf16", "f32", torch.bfloat16, torch.float32):
             raise ValueError(f"dtype: expected bf16 or f32, got {dtype}")
+        _fits(n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, head_dim=head_dim, page_size=page_size,
+              n_pages=n_pages, max_requests=max_requests, max_pages=max_pages)
         self.dtype = BF16 if dtype in ("bf16", torch.bfloat16) else F32
         self.Hq, self.Hkv, self.D, self.page_size = n_q_heads, n_kv_heads, head_dim, page_size
         self.n_pages, self.max_requests, self.max_pages = n_pages, max_requests, max_pages
@@ -620,6 +632,8 @@ class PagedStore:
         """Grows request r by n_new[r] tokens.  Returns (slots [n_slots], -1 past the new
         tokens; starts [R + 1], the first new token of each request)."""
         R = n_new.shape[0]
+        if R > _MOST or n_slots > _MOST:
+            _fits(requests=R, n_slots=n_slots)
         slots, sp = self._out("slots", slots, (n_slots,), torch.int32)
         starts, tp = self._out("starts", starts, (R + 1,), torch.int32)
         self._call("rba_paged_extend", self._arg("n_new", n_new, (R,), torch.int32), R, sp, n_slots,
@@ -629,6 +643,8 @@ class PagedStore:
     def truncate(self, keep):
         """Cuts request r back to at most keep[r] tokens (0: the request is over)."""
         R = keep.shape[0]
+        if R > _MOST:
+            _fits(requests=R)
         self._call("rba_paged_truncate", self._arg("keep", keep, (R,), torch.int32), R)
 
     # -- rows ----------------------------------------------------------------------
@@ -636,6 +652,8 @@ class PagedStore:
         """Writes rows k, v [n][Hkv][D] in 4 bits at their slots, and the mean keys of the
         pages they complete.  Rows may be strided views (a fused projection's slices)."""
         n = slots.shape[0]
+        if n > _MOST:
+            _fits(rows=n)
         kp, kt, kh = self._rows("k", k, n, self.Hkv)
         vp, vt, vh = self._rows("v", v, n, self.Hkv)
         self._call("rba_paged_append", self._arg("slots", slots, (n,), torch.int32), n, kp, kt,
@@ -644,6 +662,8 @@ class PagedStore:
     def read(self, slots, *, k=None, v=None):
         """Rows at the slots as the values held there: (k, v), each [n][Hkv][D]."""
         n = slots.shape[0]
+        if n > _MOST:
+            _fits(rows=n)
         shape = (n, self.Hkv, self.D)
         k, kp = self._out("k", k, shape, self._td)
         v, vp = self._out("v", v, shape, self._td)
@@ -659,6 +679,8 @@ class PagedStore:
         """The k best pages of each (request, kv head) for q [R][Hq][D]: idx [R][Hkv][k],
         ascending, -1 past a request's candidates."""
         R = q.shape[0]
+        if not (k <= _MOST and -1 < sink <= _MOST and -1 < window <= _MOST):
+            _fits(k=k, sink=sink, window=window)
         qp, qr, qh = self._rows("q", q, R, self.Hq)
         idx, ip = self._out("idx", idx, (R, self.Hkv, k), torch.int32)
         if workspace is None:
@@ -678,9 +700,10 @@ class PagedStore:
         R = q.shape[0]
         qp, qr, qh = self._rows("q", q, R, self.Hq)
         k = idx.shape[-1] if idx is not None else 0
+        if not (k <= _MOST and -1 < sink <= _MOST and -1 < window <= _MOST):
+            _fits(k=k, sink=sink, window=window)
         ip = self._arg("idx", idx, (R, self.Hkv, k), torch.int32) if k else None
-        if scale is None:
-            scale = 1.0 / math.sqrt(self.D)
+        scale = 1.0 / math.sqrt(self.D) if scale is None else float(scale)
         out, op = self._out("out", out, (R, self.Hq, self.D), torch.float32)
         lse, lp = self._out("lse", lse, (R, self.Hq), torch.float32)
         if workspace is None:
@@ -699,6 +722,8 @@ class PagedStore:
         buffer given it can be captured once and replayed."""
         # everything is checked before the first call: a refused step leaves the store as it was
         n, R, i32, f32 = k_new.shape[0], n_new.shape[0], torch.int32, torch.float32
+        _fits(rows=n, k=k, sink=sink, window=window)
+        scale = None if scale is None else float(scale)
         if min(k, sink, window) < 0:
             raise ValueError(f"k, sink, window: expected 0 or more, got {k}, {sink}, {window}")
         self._rows("k_new", k_new, n, self.Hkv)

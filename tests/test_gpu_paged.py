@@ -684,6 +684,30 @@ def test_a_step_with_a_workspace_off_its_boundary_grows_nothing(rba):
         assert p.st.lens.tolist() == [0, 0, 0]
 
 
+def test_numbers_past_32_bits_are_refused(rba):
+    """As 32-bit numbers 2^32 is 0: attention without its window."""
+    p = Pair(rba, 67)
+    p.grow([9, 0, 30])
+    q, qd = p.queries()
+    x = torch.ones((1, 2, 128), device="cuda").bfloat16()
+    for bad in ((2 ** 31, 0, 0), (0, 2 ** 32, 0), (0, 0, 2 ** 32), (0, 0, 2 ** 31)):
+        with pytest.raises(ValueError):
+            p.st.decode_step(qd, x, x, i32([1, 0, 0]), *bad)
+        if not bad[0]:
+            with pytest.raises(ValueError):
+                p.st.attend(qd, None, *bad[1:])
+            with pytest.raises(ValueError):
+                p.st.select(qd, 1, *bad[1:])
+    with pytest.raises(ValueError):
+        p.st.extend(i32([1, 0, 0]), 2 ** 32 + 1, slots=i32([0]))
+    with pytest.raises((TypeError, ValueError)):
+        p.st.decode_step(qd, x, x, i32([1, 0, 0]), 0, 0, 30, scale="none")
+    assert p.st.lens.tolist() == [9, 0, 30]
+    a = p.st.decode_step(qd, x, x, i32([0, 0, 0]), 0, 0, 30, scale=np.float32(0.25))
+    b = p.st.attend(qd, None, 0, 30, scale=0.25)
+    assert torch.equal(a[1], b[0]) and torch.equal(a[2], b[1])
+
+
 def test_keys_that_are_not_finite_leave_other_rows_alone(rba):
     """A page mean that is not a number makes its own row's choice unspecified, no other's."""
     for k, columns in ((3, 24), (17, 80)):  # a warp's rows, a CTA's

@@ -151,5 +151,18 @@ def test_step_check_refuses_what_a_steps_calls_would(L, store):
     L.rba_paged_destroy(h)
 
 
+def test_numbers_past_32_bits_are_refused_in_python():
+    from retrieval_block_sparse_b200.rba import PagedStore, _fits
+    for x in (2 ** 31, 2 ** 32, -2 ** 31 - 1, 2 ** 63):
+        with pytest.raises(ValueError):
+            _fits(window=x)
+    _fits(sink=0, window=2 ** 31 - 1, k=-2 ** 31)
+    sizes = dict(n_q_heads=1, n_kv_heads=1, head_dim=64, page_size=16, n_pages=2, max_requests=1,
+                 max_pages=2)
+    for name in sizes:  # (refused before anything is allocated)
+        with pytest.raises(ValueError):
+            PagedStore(**{**sizes, name: 2 ** 32 + sizes[name]})
+
+
 def test_check_wants_a_store(L):
     assert L.rba_paged_check(None, None) == INVALID
