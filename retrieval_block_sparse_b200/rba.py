@@ -511,6 +511,7 @@ class PagedStore:
       pool    uint8 [n_pages][Hkv][strips][strip_bytes]   rep   fp32 [n_pages][Hkv][P]
       table   int32 [max_requests][max_pages]             lens  int32 [max_requests]
       free    int32 [n_pages] (a stack)                   n_free int32 [1]
+    table, lens, free and n_free belong together: all of them are given, or none.
     Work runs on the store's device, on torch's current stream there.
     """
 
@@ -545,8 +546,9 @@ class PagedStore:
         def zeros(shape, dt):
             return torch.zeros(shape, dtype=dt, device=dev)
 
-        if (free is None) != (n_free is None):
-            raise ValueError("free and n_free are given together")
+        if len({t is None for t in (table, lens, free, n_free)}) > 1:
+            # (a free list made anew holds pages that the table's requests hold)
+            raise ValueError("table, lens, free and n_free are given together")
         self.pool = buf("pool", pool, (n_pages, n_kv_heads, strips, self.strip_bytes),
                         torch.uint8, zeros)
         self.rep = buf("rep", rep, (n_pages, n_kv_heads, self.pitch), torch.float32, zeros)

@@ -708,6 +708,26 @@ def test_numbers_past_32_bits_are_refused(rba):
     assert torch.equal(a[1], b[0]) and torch.equal(a[2], b[1])
 
 
+def test_tables_and_free_list_are_given_together(rba):
+    """A free list made anew beside a table in use would hand out pages that requests hold."""
+    sizes = dict(n_q_heads=2, n_kv_heads=2, head_dim=64, page_size=8, n_pages=6, max_requests=2,
+                 max_pages=4)
+    a = rba.PagedStore(**sizes)
+    a.extend(i32([9, 8]), 17)
+    own = dict(table=a.table, lens=a.lens, free=a.free, n_free=a.n_free)
+    for take in range(1, 15):  # every choice but none and all
+        with pytest.raises(ValueError):
+            rba.PagedStore(**sizes, pool=a.pool,
+                           **{n: t for i, (n, t) in enumerate(own.items()) if take >> i & 1})
+    b = rba.PagedStore(**sizes, pool=a.pool, rep=a.rep, **own)
+    slots = b.extend(i32([0, 16]), 16)[0]  # the pages that are left
+    held = a.table[0, :2].tolist() + a.table[1, :3].tolist()
+    assert len(set(held)) == 5 and a.lens.tolist() == [9, 24]
+    assert not {s // 8 for s in slots.tolist()} & set(held[:2])
+    c = rba.PagedStore(**sizes, pool=torch.zeros_like(a.pool))  # tables made for the memory given
+    assert c.lens.tolist() == [0, 0] and int(c.n_free) == 6
+
+
 def test_keys_that_are_not_finite_leave_other_rows_alone(rba):
     """A page mean that is not a number makes its own row's choice unspecified, no other's."""
     for k, columns in ((3, 24), (17, 80)):  # a warp's rows, a CTA's
