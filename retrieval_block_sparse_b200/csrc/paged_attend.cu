@@ -10,8 +10,10 @@
 // no conversion.  (Fed to the matrix unit as they are, subnormal operands cost it precision: it
 // aligns products by their nominal exponents, and the outputs were off by 2^-17.)  q is scaled by
 // a power of two per head and split into two halves (hi + lo, 22 bits); for the values the weight
-// takes the scale, w = p s_tg 2^e, split the same way.  Softmax statistics, both products'
-// accumulators and the merges are 32-bit.
+// takes the scale, w = p s_tg 2^e, split the same way, with an e for each head and group that keeps
+// the largest w in [2^7, 2^15): what a half cannot hold, 2^-25, is then at most 2^-32 of the group's
+// largest term, whatever other groups and rows without weight hold.  Softmax statistics, both
+// products' accumulators and the merges are 32-bit.
 //
 // Layout.  One warp takes a pair of strips of 16 tokens at a time.  K codes are the A operand of
 // the first product (16 tokens x 16 dims), q its B; V codes, read in token pairs, are the A operand
@@ -20,8 +22,9 @@
 // product for both); five to eight take a column each and a second product for the lo halves
 // ("wide": the accumulators stay 32 registers); larger groups are cut into chunks of eight.
 //
-// The running maximum is lazy: weights are taken relative to a reference that moves only when
-// a logit passes it by 2^4, so most strips need no cross-lane maximum and no rescale.
+// The running maximum is lazy: weights are taken relative to a reference, a whole number, that moves
+// only when a weight passes 2^4 or a w 2^15, so most strips need no cross-lane maximum and no
+// rescale.  Factors of a move are powers of two, and an e rises by what the reference rises.
 //
 // Work.  All pairs of strips of all (request, kv head) units form one line, cut evenly over
 // workers whatever the requests' lengths, each unit counted with a few pairs more for what its
@@ -34,10 +37,11 @@
 // fence and a merge by the last worker to arrive, which few warps would then wait for.  Where no
 // unit can be longer than kWholePairs, workers take whole units and there is no second kernel.
 //
-// Measured, with the merge: 4 requests of 128K tokens, 8 x 4 heads, bf16: 122.9 us, 4.9 TB/s of
-// codes and scales, 74 % of a plain copy's rate; 64 requests to 8K tokens, 4 x 8 heads, 32-bit:
-// 59 us, 2.4 TB/s.  Both are bound by the issue of 331 and about 470 instructions a strip.  8192 attended
-// tokens of one request: 12.5 us, bound by the chain launch, scan, table, copy, merge.
+// Measured, with the merge: 4 requests of 128K tokens, 8 x 4 heads, bf16: 124.3 us, 4.8 TB/s of
+// codes and scales, 73 % of a plain copy's rate (123.0 with one e for all heads and groups, which
+// lost a small group's bits to a large one's); 64 requests to 8K tokens, 4 x 8 heads, 32-bit:
+// 60.4 us (59.1), 2.4 TB/s.  Both are bound by the issue of 331 and about 470 instructions a strip.  8192 attended
+// tokens of one request: 12.9 us (12.6), bound by the chain launch, scan, table, copy, merge.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -67,8 +71,10 @@ constexpr int kWholePairs = 8;
 constexpr float kToLog2 = 1.4426950408889634f;
 constexpr float kToLn = 0.6931471805599453f;
 constexpr float kSlack = 4.f;        // a logit may pass the reference by 2^4
-constexpr int kScaleTop = 10;        // s 2^e stays below 2^10 when e is set, below 2^11 always
-constexpr int kMostE = 100, kLeastE = -118;
+constexpr int kTop = 7;              // exponent of a group's largest w when e is set
+constexpr float kMostW = 32768.f;    // a w that may reach it sets e anew
+constexpr int kMostScale = 11;       // s 2^e below 2^11 keeps w below it: 2^(11 + kSlack) = kMostW
+constexpr int kMostE = 110;          // (scales are 0 or at least 2^-100)
 
 struct PagedAttendArgs {
   const void* q;
@@ -230,30 +236,110 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {  // (a 
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
 // Parts of the q operand (in shared memory, read group by group): hi, and for wide 32-bit q lo.
 template <bool kWide, bool kLo> constexpr int q_parts() { return kWide && kLo ? 2 : 1; }
 
 // A warp's running state for the unit's heads; lane (t, c) = (lane / 4, lane % 4) holds head c
 // (packed) or heads 2 c and 2 c + 1 (wide).  A weight is 2^(y fac - m), y fac the logit in log2
-// units, fac >= 0; the values' scales are taken times 2^e, which keeps weight x scale within a
-// half's range.
+// units, fac >= 0; the values' scales are taken times 2^e, e of the head and group, which keeps
+// weight x scale within a half's range.
 template <int P, bool kWide> struct State {
   static constexpr int HL = kWide ? 2 : 1, G = P / 32;
-  float m[HL], l[HL];    // reference; this lane's part of the weights' sum
-  float top[HL];         // a logit above it moves the reference
-  float most;            // a scale above it moves e
+  float m[HL], l[HL];        // reference; this lane's part of the weights' sum
+  uint32_t up[HL][G / 2];    // 2^e of two groups to a word, as bf16
+  uint32_t most[G / 2];      // scales above it may pass kMostW with one of the heads' 2^e
   // dims 32 g + 4 t + {0, 1 (plus 16 times it), 2, 3 (the same)}: packed hi and lo columns, wide
   // two heads
   float acc[2 * G][4];
-  int e;
 };
+
+// Powers of two as bf16, two to a word: 2^n has the bits (n + 127) << 7, so words of them are added,
+// subtracted and compared as pairs of 16-bit numbers.
+constexpr uint32_t both(uint32_t x) { return x | x << 16; }
+constexpr uint32_t kFirstUp = both((kMostE + 127) << 7);
+
+template <int P, bool kWide> __device__ __forceinline__ void set_most(State<P, kWide>& st) {
+#pragma unroll
+  for (int j = 0; j < P / 64; ++j) {
+    uint32_t up = st.up[0][j];
+    if constexpr (kWide) up = __vmaxu2(up, st.up[1][j]);
+    st.most[j] = both(((kMostScale + 2 * 127) << 7) - 1) - up;  // the number below 2^(kMostScale - e)
+  }
+}
+
+// The reference moves to the largest logit so far and, for each head and group, e to where the
+// largest weight x scale asks for it: sums so far are scaled by both (first: there are none).
+// y, sv: logits and V scales of the lane's rows (-infinity and 0 for rows outside the attended set);
+// ymax, smax: their largest.
+template <int P, bool kWide, int kN>
+__device__ __forceinline__ void move_reference(const float (*y)[kN][2], const float* ymax,
+                                               const float* fac, const uint32_t (*sv)[2][P / 64],
+                                               const uint32_t* smax, bool first,
+                                               State<P, kWide>& st) {
+  constexpr int G = P / 32, HL = kWide ? 2 : 1;
+  constexpr uint32_t kExponents = both(0x7f80);
+#pragma unroll
+  for (int i = 0; i < HL; ++i) {
+    float m = ymax[i] * fac[i];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = fmaxf(st.m[i], ceilf(m));
+    const float rise = m == st.m[i] ? 0.f : m - st.m[i];  // (infinite the first time)
+    st.m[i] = m;
+    uint32_t w[G / 2];  // the largest weight x scale, in bf16 (off by one in its exponent at most)
+#pragma unroll
+    for (int j = 0; j < G / 2; ++j) w[j] = 0;
+#pragma unroll
+    for (int n = 0; n < kN; ++n)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // (-infinity times a factor of 0 is no number, and gives way)
+        const __nv_bfloat162 p = __float2bfloat162_rn(ex2(fmaf(y[i][n][half], fac[i], -m)));
+        const uint32_t p2 = *reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+        for (int j = 0; j < G / 2; ++j) w[j] = max_bf16x2(w[j], mul_bf16x2(sv[n][half][j], p2));
+      }
+    const float part = fminf(rise, 240.f), rest = ex2(part - rise);  // (an e ranges over 231)
+    const uint32_t more = both(static_cast<uint32_t>(part) << 7);
+#pragma unroll
+    for (int j = 0; j < G / 2; ++j) {
+      const uint32_t most = st.up[i][j] + more;
+      uint32_t up = __vminu2(__vminu2(most, kFirstUp),
+                             both((kTop + 2 * 127) << 7) - (w[j] & kExponents));
+      // the largest scale times 2^e stays finite, so that a weight of 0 makes it 0
+      up = __vminu2(up, both((126 + 2 * 127) << 7) - (smax[j] & kExponents));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) up = __vminu2(up, __shfl_xor_sync(0xffffffffu, up, o));
+      st.up[i][j] = up;
+      if (first) continue;
+      // sums are scaled by 2^(e - rise), an e relative to the one before: at most 1
+      const uint32_t f = both(127 << 7) - __vminu2(most - up, both(127 << 7));
+#pragma unroll
+      for (int g = 2 * j; g < 2 * j + 2; ++g) {
+        const float scale = bf16_of(&f, g & 1) * rest;
+#pragma unroll
+        for (int b = 2 * g; b < 2 * g + 2; ++b)
+#pragma unroll
+          for (int x = kWide ? i : 0; x < 4; x += kWide ? 2 : 1) st.acc[b][x] *= scale;
+      }
+    }
+    st.l[i] *= ex2(-rise);
+  }
+  set_most(st);
+}
 
 // One step: kN strips, whose rows `valid` holds (16 bits each).  The packed form takes a pair, for
 // one set of checks (123 us against 132, 128K tokens of 4 requests); a wide pair would be 13 KB of
 // instructions and short of registers (60.6 us against 58.9, 64 requests to 8K tokens).
 template <int P, bool kWide, bool kLo, int kN>
 __device__ __forceinline__ void strips_step(const uint8_t* strips, int valid, const uint32_t* qw,
-                                            const float* fac, State<P, kWide>& st) {
+                                            const float* fac, bool first, State<P, kWide>& st) {
   constexpr int G = P / 32, HL = kWide ? 2 : 1, SB = strip_bytes(P);
   const int lane = threadIdx.x & 31, t = lane >> 2;
   const bool whole = valid == (kN == 2 ? kWholePair : kWholeStrip);
@@ -311,47 +397,42 @@ __device__ __forceinline__ void strips_step(const uint8_t* strips, int valid, co
         for (int i = 0; i < HL; ++i) y[i][n][half] = -INFINITY;
       }
   }
-  // the reference moves where a logit or a scale outgrows it
-  uint32_t s2 = 0;
+  // the reference moves where a weight or weight x scale outgrows it: scales large enough for that
+  // are seen first, their rows' weights only then
+  uint32_t smax[G / 2];
 #pragma unroll
-  for (int i = 0; i < kN * 2 * (G / 2); ++i)
-    s2 = max_bf16x2(s2, sv[i / G][(i / (G / 2)) & 1][i % (G / 2)]);
-  float smax = fmaxf(bf16_of(&s2, 0), bf16_of(&s2, 1));
-  bool grow = smax > st.most;
+  for (int j = 0; j < G / 2; ++j) {
+    smax[j] = max_bf16x2(sv[0][0][j], sv[0][1][j]);
+    if constexpr (kN == 2)
+      smax[j] = max_bf16x2(smax[j], max_bf16x2(sv[kN - 1][0][j], sv[kN - 1][1][j]));
+  }
   float ymax[HL];
+  uint32_t large = 0;
+#pragma unroll
+  for (int j = 0; j < G / 2; ++j) large |= __vmaxu2(smax[j], st.most[j]) ^ st.most[j];
+  bool grow = first || large != 0;
 #pragma unroll
   for (int i = 0; i < HL; ++i) {
     ymax[i] = fmaxf(y[i][0][0], y[i][0][1]);
     if constexpr (kN == 2) ymax[i] = fmaxf(ymax[i], fmaxf(y[i][kN - 1][0], y[i][kN - 1][1]));
-    ymax[i] *= fac[i];
-    grow |= ymax[i] > st.top[i];
+    grow |= fmaf(ymax[i], fac[i], -st.m[i]) > kSlack;
   }
   if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
-    const int e = min(st.e, max(kScaleTop - 1 - exponent(smax), kLeastE));
-    const float fe = pow2(max(e - st.e, -126));
-    st.e = e;
-    st.most = pow2(kScaleTop - e);
-    float f[HL];
+    grow = first;
 #pragma unroll
     for (int i = 0; i < HL; ++i) {
-      float m = ymax[i];
+      const float over = fmaf(ymax[i], fac[i], -st.m[i]);
+      // (-infinity times a factor of 0 is no number: no weight)
+      const float p = fmaxf(ex2(over), 0.f);
+      uint32_t s = mul_bf16x2(smax[0], st.up[i][0]);
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      m = fmaxf(st.m[i], m);
-      f[i] = m == st.m[i] ? 1.f : ex2(st.m[i] - m);
-      st.m[i] = m;
-      st.top[i] = m + kSlack;
-      st.l[i] *= f[i];
-      f[i] *= fe;
+      for (int j = 1; j < G / 2; ++j) s = max_bf16x2(s, mul_bf16x2(smax[j], st.up[i][j]));
+      // (a scale that 2^e makes infinite is to be met even by a weight of 0)
+      grow |= over > kSlack || !(p * fmaxf(bf16_of(&s, 0), bf16_of(&s, 1)) < kMostW);
     }
-#pragma unroll
-    for (int b = 0; b < 2 * G; ++b)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) st.acc[b][j] *= f[kWide ? (j & 1) : 0];
+    if (__any_sync(0xffffffffu, grow))
+      move_reference<P, kWide, kN>(y, ymax, fac, sv, smax, first, st);
   }
-  const float up = pow2(st.e);
 #pragma unroll
   for (int i = 0; i < HL; ++i)
 #pragma unroll
@@ -362,14 +443,19 @@ __device__ __forceinline__ void strips_step(const uint8_t* strips, int valid, co
         // (a row without weight before any row with one: -infinity against -infinity)
         if (!whole) p = y[i][n][half] == -INFINITY ? 0.f : p;
         st.l[i] += p;
-        y[i][n][half] = p * up;
+        y[i][n][half] = p;
       }
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
-    uint32_t v[2][G];
+    uint32_t v[2][G], sc[HL][2][G / 2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int half = 0; half < 2; ++half) {
       load_words<G>(strips + n * SB + 8 * P + half * 4 * P + lane * (G * 4), v[half]);
+#pragma unroll
+      for (int i = 0; i < HL; ++i)
+#pragma unroll
+        for (int j = 0; j < G / 2; ++j) sc[i][half][j] = mul_bf16x2(sv[n][half][j], st.up[i][j]);
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       // codes of the group's two 16-dim tiles
@@ -383,10 +469,9 @@ __device__ __forceinline__ void strips_step(const uint8_t* strips, int valid, co
       float hi[HL][2], lo[HL][2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float s = bf16_of(sv[n][half], g);
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
-          const float w = y[i][n][half] * s;
+          const float w = y[i][n][half] * bf16_of(sc[i][half], g);
           hi[i][half] = __uint_as_float(__float_as_uint(w) & 0xffffe000u);
           lo[i][half] = w - hi[i][half];
         }
@@ -747,23 +832,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
     float fac[HL];
 #pragma unroll
     for (int i = 0; i < HL; ++i) fac[i] = fac_place(at_place)[HL * (lane & 3) + i];
-    // Every kFold pairs the state is added to its place in memory and starts anew: the matrix unit
+    // Every kFold pairs the sums are added to their place in memory and start anew: the matrix unit
     // cuts its sums towards zero, which over a long line would add up.
     const auto part_of = [&] { return a.parts + (int64_t(worker) * 2 + later) * S::kSlot; };
     const int t = lane >> 2, c = lane & 3;
     State<P, kWide> st;
     float4 o[HL][G];  // the warp's state in its lanes: dims 32 g + 4 t + {0..3} of heads HL c ..
     int till = min(mine, pairs_below(stop));
-    bool held = false;
+    bool held = false, first = true;
+#pragma unroll
+    for (int i = 0; i < HL; ++i) {
+      st.m[i] = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < G / 2; ++b) st.up[i][b] = kFirstUp;
+    }
+    set_most(st);
 #pragma unroll 1
     while (true) {
-      st.e = kMostE;
-      st.most = pow2(kScaleTop - kMostE);
 #pragma unroll
-      for (int i = 0; i < HL; ++i) {
-        st.m[i] = st.top[i] = -INFINITY;
-        st.l[i] = 0.f;
-      }
+      for (int i = 0; i < HL; ++i) st.l[i] = 0.f;
 #pragma unroll
       for (int b = 0; b < 2 * G; ++b)
 #pragma unroll
@@ -790,10 +877,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
 #pragma unroll 1
             for (int n = 0; n < 2; ++n) {
               const int r1 = r2 >> (16 * n) & 0xffff;
-              if (r1 != 0) strips_step<P, kWide, kLo, 1>(pair + n * SB, r1, qw, fac, st);
+              if (r1 == 0) continue;
+              strips_step<P, kWide, kLo, 1>(pair + n * SB, r1, qw, fac, first, st);
+              first = false;
             }
           } else {
-            strips_step<P, kWide, kLo, 2>(pair, r2, qw, fac, st);
+            strips_step<P, kWide, kLo, 2>(pair, r2, qw, fac, first, st);
+            first = false;
           }
         }
         __syncwarp();
@@ -801,13 +891,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(Page
       }
 
       {
-        const float down = pow2(-st.e);
 #pragma unroll
         for (int i = 0; i < HL; ++i) {
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], x);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
+            const float down = pow2(127 - static_cast<int>(st.up[i][g / 2] >> (g & 1 ? 23 : 7) & 255u));
             float y[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {

@@ -452,6 +452,94 @@ def test_attention_value_scales_far_apart(rba):
     p2.same_attention(q, qd, None, 0, 640)
 
 
+def _terms_by_group(p, q, scale):
+    """Of attention over all tokens of request 0, in fp64: (out [heads][group][dim], sum of weight x
+    largest |v| of the row's 32 dims, the same shape, bound of the logits' error, strips)."""
+    m, heads, D = p.m, p.heads, p.dim
+    rows = [m.rows[m.tables[0][t // p.page] * p.page + t % p.page] for t in range(m.lens[0])]
+    K, V = (np.stack([x[i] for x in rows], 1) for i in (0, 1))  # [heads][T][dim]
+    Q = q[0].reshape(heads, -1, D).astype(np.float64)
+    x = scale * np.einsum("hgd,htd->hgt", Q, K)
+    w = np.exp(x - x.max(-1, keepdims=True))
+    w /= w.sum(-1, keepdims=True)
+    cuts = range(0, D, 32)
+    top = lambda y: np.concatenate([np.repeat(np.abs(y[..., a:a + 32]).max(-1, keepdims=True),
+                                              len(y[0, 0, a:a + 32]), -1) for a in cuts], -1)
+    unit = max((scale * np.abs(Q) @ top(K).transpose(0, 2, 1)).max() * 15 / 7, np.abs(x).max())
+    return (np.einsum("hgt,htd->hgd", w, V), np.einsum("hgt,htd->hgd", w, top(V)),
+            24 * unit * 2.0 ** -24, m.lens[0] / 16 + 1)
+
+
+def _same_by_group(p, q, qd):
+    """Every output against its own terms: the tolerance of same_attention with the sum of a
+    group's |terms| in the place of the largest |v| of all."""
+    scale = p.dim ** -0.5
+    out = p.st.attend(qd, None, 0, 2 ** 31 - 1, scale=scale)[0]
+    p.st.check()
+    ref, terms, dx, strips = _terms_by_group(p, q, scale)
+    err = np.abs(out[0].cpu().numpy().reshape(ref.shape) - ref)
+    tol = terms * (2 * dx + 8 * 2.0 ** -22 + strips * 2.0 ** -23)
+    assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
+
+
+FORMS = [(4, 128, "f32"), (3, 128, "bf16"), (1, 64, "bf16"), (8, 100, "f32"), (5, 128, "bf16"),
+         (12, 64, "f32")]
+
+
+@pytest.mark.parametrize("group,dim,dtype", FORMS)
+@pytest.mark.parametrize("apart", [24, 32, 40])
+def test_attention_value_groups_far_apart(rba, group, dim, dtype, apart):
+    """The groups of 32 dims have scales of their own: a small one loses nothing to a large one."""
+    p = Pair(rba, 71, heads=2, group=group, dim=dim, requests=1, dtype=dtype, n_pages=64,
+             columns=60)
+    k, v = rows(p.r, (900, 2, dim), dtype), rows(p.r, (900, 2, dim), dtype)
+    for g, a in enumerate(range(0, dim, 32)):
+        v[:, 0, a:a + 32] *= np.float32(2.0 ** (-apart * (g % 2)))
+        v[:, 1, a:a + 32] *= np.float32(2.0 ** (apart * (g % 3 - 1)))
+    p.grow([900], pad=0, k=k, v=v)
+    _same_by_group(p, *p.queries())
+
+
+@pytest.mark.parametrize("group,dim,dtype", FORMS)
+@pytest.mark.parametrize("where", [0, 450, 899])
+def test_attention_huge_row_of_no_weight(rba, group, dim, dtype, where):
+    """A row whose values are 2^40 times the others' with a weight of about 2^-90 and one of 2^30
+    with about 2^-37: the other rows keep their bits."""
+    p = Pair(rba, 73, heads=2, group=group, dim=dim, requests=1, dtype=dtype, n_pages=64,
+             columns=60)
+    k, v = (rows(p.r, (900, 2, dim), dtype) for _ in range(2))
+    q = rows(p.r, (1, 2 * group, dim), dtype)
+    q[..., 0], q[..., 1:32], k[..., 0] = 16.0, 0.0, 0.0
+    for at, down, up in ((where, 62.0, 40), ((where + 100) % 900, 26.0, 30)):
+        k[at] = 0
+        k[at, :, 0] = -down * dim ** 0.5 / 16
+        v[at] *= np.float32(2.0 ** up)
+    if dtype == "bf16":
+        k = bf16(k)
+    p.grow([900], pad=0, k=k, v=v)
+    _same_by_group(p, q, cuda(q, dtype))
+
+
+@pytest.mark.parametrize("group,dim,dtype", FORMS)
+@pytest.mark.parametrize("rising", [True, False])
+def test_attention_weights_against_values(rba, group, dim, dtype, rising):
+    """Weights that rise (fall) by 2^0.1 a row and values that fall (rise) by as much: every row's
+    term counts alike, however far the reference and the scales have moved."""
+    p = Pair(rba, 79, heads=2, group=group, dim=dim, requests=1, dtype=dtype, n_pages=64,
+             columns=60)
+    T = 900
+    k, v = np.zeros((T, 2, dim), np.float32), rows(p.r, (T, 2, dim), dtype)
+    q = rows(p.r, (1, 2 * group, dim), dtype)
+    q[..., 0], q[..., 1:32] = 1.0, 0.0
+    ramp = np.arange(T) if rising else np.arange(T)[::-1]
+    k[:, :, 0] = (0.1 * math.log(2) * dim ** 0.5 * ramp)[:, None]
+    v *= (2.0 ** (-0.1 * ramp + 45)).astype(np.float32)[:, None, None]
+    if dtype == "bf16":
+        k, v = bf16(k), bf16(v)
+    p.grow([T], pad=0, k=k, v=v)
+    _same_by_group(p, q, cuda(q, dtype))
+
+
 def test_attention_one_token_dominates(rba):
     p = Pair(rba, 19, heads=2, group=4, dim=64, requests=1, dtype="f32", n_pages=64,
              columns=40)
