@@ -492,10 +492,12 @@ rba_status rba_decode_step_host(const rba_store* store, const void* q_host, void
  *   finite; a nibble is c + 8 with c = rint(x * fl(1 / s)) clamped to -7 .. 7 (0 where s is 0 or
  *   NaN), all in correctly rounded 32-bit arithmetic.  It stands for the value s c.
  *
- * Candidates: page j of a request of T tokens is a candidate when it is full and meets
- * [sink, w0), w0 = min(max(T - window, 0), page_size * (T / page_size)): the window always
- * covers a partial last page.  The attended set is sink U selected pages U window, each token
- * once.  A request of no tokens is a valid one.
+ * Candidates, as rba_candidates counts them: page j of a request of T tokens is a candidate when it
+ * is full, (j + 1) page_size > sink and j page_size < w0, w0 = min(max(T - window, 0),
+ * page_size * (T / page_size)): the window always covers a partial last page.  (A page that the
+ * sink ends in and the window begins in before that is a candidate without a token of its own.)
+ * The attended set is sink U selected pages U window, each token once.  A request of no tokens is a
+ * valid one.
  *
  * Rows of q and of new K / V have dense dims and any row strides (in elements).  Calls that
  * change a store (extend, truncate, append) are ordered by the caller against each other and

@@ -58,8 +58,8 @@ __device__ __forceinline__ int div(int x, const FastDiv& f) {
   return f.d <= 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), f.m) >> f.s);
 }
 
-// One request's attended set, in strips.  Page j is a candidate when it is full and
-// meets [sink, w0); the window always covers the partial last page.
+// One request's attended set, in strips.  Page j is a candidate when it is full, ends past sink and
+// begins before w0; the window always covers the partial last page.
 struct PagedGeo {
   int T, w0, sink_end, first, nc;
 };

@@ -358,6 +358,17 @@ def test_selection_ties_go_to_the_lower_page(rba):
         assert np.array_equal(got.cpu().numpy(), p.m.select(q, k, 0, 0)), k
 
 
+def test_a_candidate_between_sink_and_window(rba):
+    """The window begins before the sink ends, in one page: a candidate, of no token of its own."""
+    p = Pair(rba, 83, page=128, n_pages=4, requests=2, columns=3)
+    p.grow([200, 100])
+    q, qd = p.queries()
+    assert p.m.parts(0, 100, 150) == (50, 50, [0])
+    idx = p.st.select(qd, 2, 100, 150)
+    assert idx.tolist() == [[[0, -1]] * 2, [[-1, -1]] * 2]
+    p.same_attention(q, qd, idx.cpu().numpy(), 100, 150)
+
+
 # ---------------------------------------------------------------------------------------------
 # attention
 
