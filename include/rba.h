@@ -593,7 +593,10 @@ size_t rba_paged_select_workspace_size(const rba_paged* store);
 /* Decode attention of one token of each request r < n_requests over its attended set:
  *   out = sum_t softmax_t(scale * q . k_t) v_t, lse the natural log of the sum;
  * zeros and -infinity for a request of no tokens.  (Stored keys of 2^112 and more in size can
- * overflow a logit's partial sums whatever q is.)
+ * overflow a logit's partial sums whatever q is.)  Sums are 32-bit; an element of q counts to within
+ * 2^-22 of itself or 2^-39 of its head's largest, whichever is more, and a softmax weight times a
+ * row's value scale to within 2^-22 of itself or 2^-32 of the largest such term of its head and 32
+ * dims.
  *   idx  device int32 [n_requests][Hkv][k] as rba_paged_select writes it (NULL when k = 0): the
  *        first min(k, candidates) entries, distinct, are attended; others are not read.  An
  *        entry that is no candidate is skipped and flagged.  k = 0 with a window of at least

@@ -1200,7 +1200,8 @@ extern "C" rba_status rba_paged_attend(const rba_paged* s, const void* q,
             ((q_request_stride | q_head_stride) & 3) == 0;
   a.first = sink / a.bs;
   // the longest unit there can be: what sink, selection and window ask for (each may begin and end
-  // inside a page), or the whole table
+  // inside a page), or the whole table.  (A page that two of them share is counted once here, so a
+  // unit of a short table can be two pages longer than kWholePairs: that costs its warp time only.)
   const auto strips_of = [&](int n) { return int64_t(n / a.bs) * s->strips + n % a.bs / kStrip; };
   const int64_t strips =
       std::min(strips_of(sink) + (int64_t(k) + 4) * s->strips + strips_of(window),

@@ -221,6 +221,53 @@ def test_rows_are_stored_bit_by_bit(rba, heads, dim, page, dtype):
         assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("heads,dim,page,dtype,n", [(64, 64, 16, "bf16", 40), (32, 100, 50, "f32", 90),
+                                                    (24, 128, 7, "bf16", 131),
+                                                    (40, 36, 33, "f32", 61)])
+@pytest.mark.parametrize("scattered", [True, False])
+def test_rows_of_many_heads_are_stored_bit_by_bit(rba, heads, dim, page, dtype, n, scattered):
+    """More (row, head) pairs than a CTA each: slots in no order, alone, in runs up and down, or all
+    in a row, -1 between them."""
+    r = np.random.default_rng(n)
+    n_pages = -(-4 * n // page)
+    st = rba.PagedStore(n_q_heads=heads, n_kv_heads=heads, head_dim=dim, page_size=page,
+                        n_pages=n_pages, max_requests=1, max_pages=n_pages, dtype=dtype)
+    free = r.permutation(n_pages * page // 4)[:n // 2] * 4  # one row of four each
+    run = np.arange(n - n // 2) // 2 * 4 + 1 + np.arange(n - n // 2) % 2  # two rows beside them
+    slots = np.concatenate([free, run[::-1][:len(run) // 3], run[:len(run) - len(run) // 3]])
+    if not scattered:
+        slots = np.arange(5, 5 + n)
+    slots[5::11 if scattered else 57] = -1
+    k, v = (rows(r, (n, heads, dim), dtype) for _ in range(2))
+    if dtype == "bf16":
+        k, v = bf16(k), bf16(v)
+    st.pool.fill_(0xA5)
+    st.append(i32(slots), cuda(k, dtype), cuda(v, dtype))
+    st.check()
+    kept = {int(s): i for i, s in enumerate(slots) if s >= 0}
+    assert len(kept) == (slots >= 0).sum()
+    pool = st.pool.cpu().numpy()
+    for page_no in range(n_pages):
+        for s in range(-(-page // 16)):
+            own = [kept.get(page_no * page + s * 16 + t) if s * 16 + t < page else None
+                   for t in range(16)]
+            if all(i is None for i in own):
+                assert (pool[page_no, :, s] == 0xA5).all()
+                continue
+            for h in r.permutation(heads)[:6]:
+                image, mask = O.strip_image(
+                    *([None if i is None else O.quantise_row(x[i, h]) for i in own]
+                      for x in (k, v)), st.pitch)
+                want = (image & mask) | (0xA5 & ~mask)
+                assert np.array_equal(pool[page_no, h, s], want), (page_no, h, s)
+    # the other heads hold their own rows too
+    got = st.read(i32(list(kept)))
+    for x, y in zip((k, v), got):
+        want = np.stack([[O.row_values(*O.quantise_row(x[i, h])) for h in range(heads)]
+                         for i in kept.values()])
+        assert torch.equal(y.cpu(), torch.from_numpy(want).float().to(y.dtype))
+
+
 def test_special_values(rba):
     p = Pair(rba, 9, heads=1, dim=128, page=16, dtype="f32", requests=1)
     k = rows(p.r, (8, 1, 128))
@@ -551,6 +598,33 @@ def test_attention_weights_against_values(rba, group, dim, dtype, rising):
     _same_by_group(p, q, cuda(q, dtype))
 
 
+@pytest.mark.parametrize("group,dim,dtype", FORMS)
+@pytest.mark.parametrize("apart", [20, 28])
+def test_attention_query_elements_far_apart(rba, group, dim, dtype, apart):
+    """Small elements of q against large keys, large ones against small: logits to within what rba.h
+    states, 2^-39 of a head's largest element an element beside the bound of same_attention."""
+    p = Pair(rba, 89, heads=2, group=group, dim=dim, requests=1, dtype=dtype, n_pages=64,
+             columns=60)
+    k, q = rows(p.r, (300, 2, dim), dtype), rows(p.r, (1, 2 * group, dim), dtype)
+    for g, a in enumerate(range(0, dim, 32)):
+        by = np.float32(2.0 ** ((apart // 2) * (-1) ** g))
+        q[..., a:a + 32] *= by
+        k[..., a:a + 32] /= by
+    p.grow([300], pad=0, k=k)
+    qd = cuda(q, dtype)
+    scale = dim ** -0.5
+    out, lse = p.st.attend(qd, None, 0, 300, scale=scale)
+    p.st.check()
+    ref, rl, vmax, unit = p.m.attend(q, None, 0, 300, scale)
+    held = np.stack([x[0] for x in p.m.rows.values()])
+    most = max(np.abs(held[:, h]).sum(-1).max() * np.abs(q[0, h * group:(h + 1) * group]).max()
+               for h in range(2))
+    dx = 24 * unit * 2.0 ** -24 + scale * most * 2.0 ** -39
+    tol = vmax * (2 * dx + 8 * 2.0 ** -22 + 20 * 2.0 ** -23)
+    assert np.abs(out.cpu().numpy() - ref).max() <= tol
+    assert np.abs(lse.cpu().numpy() - rl).max() <= dx + (np.abs(rl).max() + 4) * 2.0 ** -22
+
+
 def test_attention_one_token_dominates(rba):
     p = Pair(rba, 19, heads=2, group=4, dim=64, requests=1, dtype="f32", n_pages=64,
              columns=40)
@@ -717,6 +791,53 @@ def test_readers_on_two_streams(rba):
     torch.cuda.synchronize()
     for out, lse, s in got:
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(s, sel)
+
+
+def test_decode_step_captured_and_replayed(rba):
+    """The whole step in one graph with every buffer given, against the same calls made one by one on
+    a second store, while requests grow, stay, end and start again."""
+    a, b = (Pair(rba, 97, heads=2, group=4, dim=64, page=8, n_pages=60, columns=24)
+            for _ in range(2))
+    for p in (a, b):
+        p.grow([70, 0, 33])
+    st, k, sink, window = a.st, 3, 5, 20
+    new = i32([0, 0, 0])
+    kv = torch.zeros((4, 2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((3, 8, 64), dtype=torch.bfloat16, device="cuda")
+    f32 = dict(dtype=torch.float32, device="cuda")
+    own = dict(slots=i32([0] * 4), starts=i32([0] * 4), idx=i32(np.zeros((3, 2, k))),
+               out=torch.empty((3, 8, 64), **f32), lse=torch.empty((3, 8), **f32),
+               select_workspace=st.select_workspace(), workspace=st.attend_workspace())
+
+    def step():
+        return st.decode_step(q, kv[:, 0], kv[:, 1], new, k, sink, window, **own)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()  # a first call of each kernel before the capture: no request grows
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    assert [t.data_ptr() for t in got] == [own[n].data_ptr() for n in ("idx", "out", "lse")]
+    for i in range(24):
+        grow = [1, int(i % 3 == 1), 2]
+        if i == 13:
+            for p in (a, b):
+                p.st.truncate(i32([2 ** 31 - 1, 0, 40]))
+        new.copy_(i32(grow))
+        kv.copy_(torch.stack([cuda(rows(a.r, (4, 2, 64), "bf16")) for _ in range(2)], 1))
+        q.copy_(cuda(rows(a.r, (3, 8, 64), "bf16")))
+        graph.replay()
+        slots, _ = b.st.extend(new, 4)
+        b.st.append(slots, kv[:, 0], kv[:, 1])
+        idx = b.st.select(q, k, sink, window)
+        want = (idx, *b.st.attend(q, idx, sink, window))
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), i
+        assert torch.equal(own["slots"], slots) and torch.equal(st.lens, b.st.lens)
+        assert torch.equal(st.pool, b.st.pool) and torch.equal(st.rep, b.st.rep)
+        st.check()
 
 
 def test_decode_step_is_the_four_calls(rba):
