@@ -415,8 +415,15 @@ RowArgs row_args(const rba_paged* s, const int32_t* slots, int n) {
   a.bs = s->d.page_size;
   a.strips = s->strips;
   a.n_pages = s->d.n_pages;
-  // a CTA per slot and head while that is at most one wave; else fewer CTAs look through more slots
-  a.window = int64_t(n) * a.heads <= int64_t(num_sms()) * 16 ? 1 : 16;
+  // The fewest slots a CTA (up to 16, a whole strip's) with which the grid is at most one wave: its
+  // runs go one after another, and rows far apart are a run each.  us, single rows far apart / rows
+  // in a row, 8 bf16 heads of 128, with 1, 2, 4, 8, 16 slots a CTA:
+  //    297 rows   8.0 / 6.3    9.3 / 5.9   11.8 / 6.1   14.3 / 5.8   20.9 / 6.7
+  //   1024       17.6 / 12.4  17.2 / 8.8   18.5 / 7.8   22.5 / 7.5   35.8 / 8.4
+  //   8192        112 / 73.9  99.6 / 40.4  95.5 / 24.3  94.8 / 18.2  99.5 / 16.5
+  a.window = 1;
+  while (a.window < kStrip && int64_t(n) * a.heads > int64_t(num_sms()) * 16 * a.window)
+    a.window *= 2;
   a.by_bs = fast_div(a.bs);
   a.by_heads = fast_div(a.heads);
   return a;
