@@ -656,6 +656,26 @@ def test_values_that_are_not_finite_stay_in_their_place(rba):
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("group,dim,dtype", FORMS)
+def test_queries_that_are_not_finite_leave_other_heads_alone(rba, group, dim, dtype):
+    p = Pair(rba, 101, heads=2, group=group, dim=dim, requests=2, dtype=dtype, n_pages=64,
+             columns=60)
+    p.grow([500, 37])
+    q, qd = p.queries()
+    bad = np.zeros(q.shape[:2], bool)
+    for r, h, x in ((0, 0, np.nan), (0, 2 * group - 1, np.inf), (1, group, -np.inf)):
+        qd[r, h, 5] = float(x)
+        bad[r, h] = True
+    out, lse = (x.cpu().numpy() for x in p.st.attend(qd, None, 4, 300, scale=dim ** -0.5))
+    p.st.check()
+    ref, rl, vmax, unit = p.m.attend(q, None, 4, 300, dim ** -0.5)
+    dx = 24 * unit * 2.0 ** -24
+    tol = vmax * (2 * dx + 8 * 2.0 ** -22 + 33 * 2.0 ** -23)
+    assert np.abs(out - ref)[~bad].max(initial=0) <= tol
+    assert np.abs(lse - rl)[~bad].max(initial=0) <= dx + (np.abs(rl).max() + 4) * 2.0 ** -22
+    assert not np.isfinite(out[bad]).any()
+
+
 def test_strided_queries(rba):
     p, idx, sink, window = _attended(rba, 29, ATTEND[0])
     q, qd = p.queries()
@@ -1030,6 +1050,56 @@ def test_lines_of_every_kind(rba, case):
         want = torch.logsumexp(x, -1).flatten()
         tol = 24 * unit * 2.0 ** -24 + (want.abs().max().item() + 4) * 2.0 ** -22
         assert (lse[i].double() - want).abs().max().item() <= tol, i
+
+
+@pytest.mark.parametrize("group,dtype", [(2, "bf16"), (8, "f32")])
+def test_as_many_requests_as_a_table_holds(rba, group, dtype):
+    """4096 requests of 0 to 71 tokens: select, attend and read against torch in 64 bits."""
+    R, page, D, sink, window, k = 4096, 8, 64, 3, 20, 2
+    shape = dict(n_q_heads=group, n_kv_heads=1, head_dim=D, page_size=page, n_pages=R * 9,
+                 max_requests=R, max_pages=9)
+    st = rba.PagedStore(**shape, dtype=dtype)
+    torch.manual_seed(5)
+    lens = torch.randint(0, 72, (R,), device="cuda").int()
+    n = int(lens.sum())
+    kv = torch.randn((n, 2, 1, D), device="cuda").to(st.tdtype)
+    slots, starts = st.extend(lens, n)
+    st.append(slots, kv[:, 0], kv[:, 1])
+    q = torch.randn((R, group, D), device="cuda").to(st.tdtype)
+    idx = st.select(q, k, sink, window)
+    out, lse = st.attend(q, idx, sink, window)
+    st.check()
+    assert torch.equal(st.lens, lens) and int(starts[-1]) == n
+    wide = rba.PagedStore(**shape, dtype="f32", pool=st.pool, rep=st.rep, table=st.table,
+                          lens=st.lens, free=st.free, n_free=st.n_free)
+    K, V = (torch.zeros((R, 72, D), dtype=torch.float64, device="cuda") for _ in range(2))
+    r = torch.repeat_interleave(torch.arange(R, device="cuda"), lens.long())
+    t = torch.arange(n, device="cuda") - starts[:-1].long()[r]
+    for x, y in zip((K, V), wide.read(slots)):
+        x[r, t] = y[:, 0].double()
+    L, pos, j = lens.long()[:, None], torch.arange(72, device="cuda"), torch.arange(9, device="cuda")
+    w0 = torch.minimum((L - window).clamp(min=0), L // page * page)
+    cand = (j < L // page) & ((j + 1) * page > sink) & (j * page < w0)
+    Q = q.double()
+    score = torch.einsum("rd,rjd->rj", Q.sum(1), st.rep[st.table.long().clamp(min=0), 0, :D].double())
+    score = score.float().masked_fill(~cand, -math.inf)
+    best = score.sort(descending=True, stable=True).indices[:, :k]
+    best = torch.where(torch.gather(cand, 1, best), best, 99).sort().values
+    assert torch.equal(idx[:, 0].long(), torch.where(best == 99, -1, best))
+    chosen = (best[:, :, None] == j).any(1)
+    seen = (pos < L) & ((pos < torch.minimum(w0, torch.tensor(sink, device="cuda"))) | (pos >= w0) |
+                        chosen.repeat_interleave(page, 1))
+    x = (torch.einsum("rgd,rtd->rgt", Q, K) * D ** -0.5).masked_fill(~seen[:, None], -math.inf)
+    some = seen.any(1)
+    ref = torch.einsum("rgt,rtd->rgd", x.softmax(-1).nan_to_num(0.0), V)
+    assert not out[~some].any() and torch.isneginf(lse[~some]).all() and (~some).any()
+    unit = (Q.abs().sum(-1).max() * K.abs().max() * D ** -0.5 * 15 / 7).item()
+    dx = 24 * unit * 2.0 ** -24
+    tol = V.abs().max().item() * (2 * dx + 8 * 2.0 ** -22 + 6 * 2.0 ** -23)
+    assert (out.double() - ref).abs().max().item() <= tol
+    want = torch.logsumexp(x, -1)[some]
+    assert (lse[some].double() - want).abs().max().item() <= dx + (
+        want.abs().max().item() + 4) * 2.0 ** -22
 
 
 @pytest.mark.parametrize("heads,group,page,k,requests", [(2, 1, 16, 3, 40), (1, 3, 8, 16, 9),
