@@ -1052,6 +1052,44 @@ def test_lines_of_every_kind(rba, case):
         assert (lse[i].double() - want).abs().max().item() <= tol, i
 
 
+def test_offsets_past_32_bits(rba):
+    """Pages past 4 GB of the pool and rows 2^31 elements apart: bit for bit what a small store on
+    dense rows gives."""
+    heads, page, D, n = 8, 128, 128, 700
+    sizes = dict(n_q_heads=16, n_kv_heads=heads, head_dim=D, page_size=page, max_requests=2,
+                 max_pages=8)
+    many = 2 ** 32 // (heads * page // 16 * 2304) + 100
+    def order(n_pages):
+        return dict(table=torch.full((2, 8), -1, dtype=torch.int32, device="cuda"),
+                    lens=i32([0, 0]), n_free=i32([n_pages]),
+                    free=torch.arange(n_pages, dtype=torch.int32, device="cuda"))
+    a = rba.PagedStore(**sizes, n_pages=many, **order(many))
+    b = rba.PagedStore(**sizes, n_pages=8, **order(8))
+    torch.manual_seed(3)
+    k, v = (torch.randn((n, heads, D), device="cuda").bfloat16() for _ in range(2))
+    far = torch.empty(2 ** 32 + 4 * heads * D, dtype=torch.bfloat16, device="cuda")
+    kf, vf = (far.as_strided((3, heads, D), (2 ** 31, D, 1), at) for at in (0, heads * D))
+    kf.copy_(k[-3:])
+    vf.copy_(v[-3:])
+    q = torch.randn((2, 16, D), device="cuda").bfloat16()
+    qf = far.as_strided((2, 16, D), (2 ** 32, D, 1), 2 * heads * D)
+    qf.copy_(q)
+    got = []
+    for st, rows, Q in ((a, ((k[:-3], v[:-3]), (kf, vf)), qf), (b, ((k, v),), q)):
+        slots, _ = st.extend(i32([400, 300]), n)
+        at = 0
+        for x, y in rows:
+            st.append(slots[at:at + len(x)], x, y)
+            at += len(x)
+        assert at == n and int(st.table[0, 0]) == st.n_pages - 1
+        idx = st.select(Q, 1, 130, 100)
+        got.append((idx, *st.attend(Q, idx, 130, 100), *st.read(slots)))
+        st.check()
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert torch.equal(a.pool[-8:], b.pool) and torch.equal(a.rep[-8:], b.rep)
+    assert not a.pool[:8].any()
+
+
 @pytest.mark.parametrize("group,dtype", [(2, "bf16"), (8, "f32")])
 def test_as_many_requests_as_a_table_holds(rba, group, dtype):
     """4096 requests of 0 to 71 tokens: select, attend and read against torch in 64 bits."""
