@@ -40,8 +40,12 @@
 // Measured, with the merge: 4 requests of 128K tokens, 8 x 4 heads, bf16: 124.3 us, 4.8 TB/s of
 // codes and scales, 73 % of a plain copy's rate (123.0 with one e for all heads and groups, which
 // lost a small group's bits to a large one's); 64 requests to 8K tokens, 4 x 8 heads, 32-bit:
-// 60.4 us (59.1), 2.4 TB/s.  Both are bound by the issue of 331 and about 470 instructions a strip.  8192 attended
-// tokens of one request: 12.9 us (12.6), bound by the chain launch, scan, table, copy, merge.
+// 60.4 us (59.1), 2.4 TB/s.  335 and 510 instructions a strip (starts and ends of units included)
+// keep 63 and 56 % of the issue slots busy: neither issue nor memory is full, the rest is warps that
+// wait for a math pipe, for fixed latencies, for dispatch, and the wide form for code (16 warps an
+// SM, 128 registers each: no more fit; the forms of 128 dims spill 12 to 56 bytes).  The same 4 x 128K in 32 bits: 124.1 us; with eight q heads to a kv head 165 (bf16) and
+// 181 us (32-bit).  8192 attended tokens of one request: 12.9 us (12.6), bound by the chain launch,
+// scan, table, copy, merge.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -58,7 +62,7 @@ constexpr int kCtasPerSm = 2;
 constexpr int kStages = 2;  // pairs of strips in a warp's ring (pair n takes place n % 2)
 // What a unit's start and end cost, in pairs of its worker: a CTA's, a single warp's; and the pairs
 // that a warp working alone takes at least (or a whole unit).  A CTA takes a multiple of kWarps, so
-// that its warps have the same number: one each at 8192 of 128K tokens (8 kv heads) takes 12.6 us,
+// that its warps have the same number: one each at 8192 of 128K tokens (8 kv heads) took 12.6 us,
 // two each 14.3, 18 pairs to eight warps 14.8.
 constexpr int kTeamCost = 10, kAloneCost = 3;
 constexpr int kAloneLeast = 2;

@@ -9,8 +9,9 @@
 // 7 * 2^-9 of a step.  Every operation is a correctly rounded 32-bit one, so the codes are a
 // function of the inputs alone.
 //
-// All three kernels are bound by the issue of instructions: 8192 tokens of 8 heads of 128 in bf16
-// take 16 us to append, the means with it (43 MB), and 9.6 us to read back (43 MB, 4.5 TB/s).
+// All three kernels are bound by the issue of instructions (56 to 75 % of its slots): 8192 tokens of 8
+// heads of 128 in bf16 take 16.6 us to append, the means with it (43 MB), and 9.4 us to read back
+// (43 MB, 4.6 TB/s); in 32 bits 20.7 and 12.1 us (77 MB).
 #include "paged.cuh"
 
 namespace rba {
@@ -244,7 +245,8 @@ __device__ __forceinline__ void for_runs(const RowArgs& a, int h, int64_t base, 
 // One CTA per (window of slots, head) writes the window's runs, a warp to each half strip of K and
 // of V.  A whole strip is put together in shared memory and leaves it in 16-byte pieces; a part of
 // one goes out unit by unit (the rows beside it belong to other calls).
-// (Eight bf16 rows fit 40 registers a thread, 48 warps an SM; 32-bit rows take 64.)
+// (Eight bf16 rows fit 40 registers a thread, 48 warps an SM, with 40 bytes spilled, and are faster so
+// than with 48 or 64; 32-bit rows take 64.)
 template <int P> constexpr int run_warps() { return P == 128 ? 4 : 2; }
 template <typename T, int P>
 __global__ void __launch_bounds__(run_warps<P>() * 32,

@@ -3,7 +3,8 @@
 // score(r, h, j) = sum over dims of (sum over the group's q heads of q) * rep[table[r][j]][h] for
 // request r's candidate pages j, rounded once to 32 bits; the k best per (request, kv head), ties
 // to the lower page.  A 32-bit accumulation would leave the order of near pages to the order of the
-// sum, so it is held in 64.  (In two 32-bit words, with exact products and sums, the same bits cost
+// sum, so it is held in 64.  (Only candidates near the k-th place need that; the others are summed so
+// too, to have one pass.  In two 32-bit words, with exact products and sums, the same bits cost
 // a fifth more time at 86 MB of page means: five times the instructions.)
 #include "paged.cuh"
 #include "paged_ring.cuh"

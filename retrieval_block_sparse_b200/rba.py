@@ -721,7 +721,9 @@ class PagedStore:
         """One step of every request: request r grows by n_new[r] tokens, whose rows are packed in
         k_new, v_new [n][Hkv][D] (n may be larger: rows past them are ignored), then q [R][Hq][D]
         attends to sink, its k best pages and window.  Returns (idx, out, lse).  With every
-        buffer given it can be captured once and replayed."""
+        buffer given it can be captured once and replayed.  A step refused with an exception has
+        changed nothing; one whose extension the device refuses (too few free pages) writes no row,
+        attends to what is held, and is reported by check()."""
         # everything is checked before the first call: a refused step leaves the store as it was
         n, R, i32, f32 = k_new.shape[0], n_new.shape[0], torch.int32, torch.float32
         _fits(rows=n, k=k, sink=sink, window=window)
