@@ -43,9 +43,10 @@
 // 60.4 us (59.1), 2.4 TB/s.  335 and 510 instructions a strip (starts and ends of units included)
 // keep 63 and 56 % of the issue slots busy: neither issue nor memory is full, the rest is warps that
 // wait for a math pipe, for fixed latencies, for dispatch, and the wide form for code (16 warps an
-// SM, 128 registers each: no more fit; the forms of 128 dims spill 12 to 56 bytes).  The same 4 x 128K in 32 bits: 124.1 us; with eight q heads to a kv head 165 (bf16) and
-// 181 us (32-bit).  8192 attended tokens of one request: 12.9 us (12.6), bound by the chain launch,
-// scan, table, copy, merge.
+// SM, 128 registers each: no more fit; the forms of 128 dims spill 12 to 56 bytes).  The same
+// 4 x 128K in 32 bits: 124.1 us; with eight q heads to a kv head 165 (bf16) and 181 us (32-bit).
+// 8192 attended tokens of one request: 12.9 us (12.6), bound by the chain launch, scan, table, copy,
+// merge.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -333,7 +334,8 @@ __device__ __forceinline__ void move_reference(const float (*y)[kN][2], const fl
           for (int x = kWide ? i : 0; x < 4; x += kWide ? 2 : 1) st.acc[b][x] *= scale;
       }
     }
-    st.l[i] *= ex2(-rise);
+    const uint32_t down = both(127 << 7) - __vminu2(more, both(127 << 7));
+    st.l[i] *= bf16_of(&down, 0) * rest;
   }
   set_most(st);
 }
